@@ -1,0 +1,660 @@
+"""Measured cases of the operators between a training step's FP8 GEMMs.
+
+Three operators, each forward and backward:
+
+* layer norm ("ln_fwd", "ln_bwd"): the forward pass with its output as BF16
+  and/or as an FP8 GEMM operand and its normalised rows as an 8-bit
+  checkpoint; the backward pass from x or from that checkpoint, with the
+  reduction of the gradients of gamma and beta;
+* activations with 8-bit checkpoints ("act_fwd", "act_bwd", "ckpt"): GELU,
+  SiLU and their gated forms, the input kept in 8 bits and the backward pass
+  computed from it (which also recomputes the output for the next weight
+  gradient); saving and loading a checkpoint by itself;
+* tokens sorted by expert ("moe_route", "moe_combine", "moe_combine_bwd"): the
+  stable sort with padded segments, the gather of the token rows (as BF16 or
+  as an FP8 GEMM operand), the weighted sum back, and the gradients.
+
+``own`` selects the side: False, the formulas in elementary torch operations
+in 32 bits; True, the calls of ``scaled_fp8_gemm_amd.fp8sg``.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+DEV = "cuda" if torch.cuda.is_available() else "cpu"
+FMAX = 448.0                 # largest E4M3 value
+FLT_MAX = torch.finfo(torch.float32).max
+EPS = 1e-5
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+# ------------------------------------------------------------------ cases
+def listed():
+    return [
+        # one decode-sized batch of rows through the norm: latency
+        {"name": "ln_fwd 8x4096", "op": "ln_fwd", "rows": 8, "cols": 4096, "x": "bf16",
+         "w": "f32", "y": True, "yq": "none", "ckpt": False},
+        # the norm in front of the GPT-175B MLP share's MXFP8 GEMM: FP8 operand
+        # and 8-bit checkpoint, no BF16 output
+        {"name": "ln_fwd 4096x12288 mx ckpt", "op": "ln_fwd", "rows": 4096, "cols": 12288,
+         "x": "bf16", "w": "f32", "y": False, "yq": "mx", "ckpt": True},
+        # its counterpart at the 13B width: backward from the 8-bit checkpoint
+        {"name": "ln_bwd 8192x5120 ckpt", "op": "ln_bwd", "rows": 8192, "cols": 5120,
+         "x": "bf16", "w": "f32", "ckpt": True},
+        # an FP32 residual stream of an odd width
+        {"name": "ln_bwd 1000x1003 f32", "op": "ln_bwd", "rows": 1000, "cols": 1003,
+         "x": "f32", "w": "bf16", "ckpt": False},
+        # the 7B MLP's gate between its GEMMs under the blockwise recipe
+        {"name": "swiglu_fwd 4096x11008 block", "op": "act_fwd", "rows": 4096, "cols": 11008,
+         "act": "silu", "gated": True, "y": False, "yq": "block", "ckpt": True},
+        # the GPT-175B share's GELU, backward from its 8-bit checkpoint, with
+        # the output recomputed for the second weight gradient (the largest)
+        {"name": "gelu_bwd 4096x49152 ckpt", "op": "act_bwd", "rows": 4096, "cols": 49152,
+         "act": "gelu_tanh", "gated": False, "ckpt": True, "y": True},
+        # a short ragged batch of an odd width
+        {"name": "swiglu_bwd 333x1001 ckpt", "op": "act_bwd", "rows": 333, "cols": 1001,
+         "act": "silu", "gated": True, "ckpt": True, "y": False},
+        # an activation stored in 8 bits and brought back
+        {"name": "ckpt 8192x4096", "op": "ckpt", "rows": 8192, "cols": 4096},
+        # one expert-parallel rank's tokens to 8 experts, blockwise operand
+        {"name": "moe_route 8192x4096 e8k2", "op": "moe_route", "tokens": 8192, "cols": 4096,
+         "experts": 8, "k": 2, "pad": 128, "xq": "block"},
+        # a decode step's tokens to 8 experts: latency
+        {"name": "moe_route 16x4096 e8k2", "op": "moe_route", "tokens": 16, "cols": 4096,
+         "experts": 8, "k": 2, "pad": 16, "xq": "none"},
+        # the experts' outputs back, fine-grained experts
+        {"name": "moe_combine 4096x4096 e64k6", "op": "moe_combine", "tokens": 4096,
+         "cols": 4096, "experts": 64, "k": 6, "pad": 128},
+        # and the gradient of that sum
+        {"name": "moe_combine_bwd 8192x5120 e8k2", "op": "moe_combine_bwd", "tokens": 8192,
+         "cols": 5120, "experts": 8, "k": 2, "pad": 128},
+    ]
+
+
+def _size(rng, lo, hi, step):
+    """A size spread over the logarithm of [lo, hi]: odd, or an odd multiple of step."""
+    n = int(math.exp(rng.uniform(math.log(lo), math.log(hi))))
+    return max(1, n | 1) if rng.random() < 0.5 else step * max(1, (n // step) | 1)
+
+
+def draw(rng):
+    op = rng.choice(["ln_fwd", "ln_bwd", "act_fwd", "act_bwd", "ckpt", "moe_route",
+                     "moe_combine", "moe_combine_bwd"])
+    if op.startswith("moe"):
+        k = rng.choice([1, 2, 4, 6, 8])
+        experts = rng.choice([8, 16, 40, 64, 128])
+        cols = _size(rng, 64, 8192, 128)
+        tokens = min(_size(rng, 1, 16384, 16), max(1, (1 << 26) // (k * cols)))
+        c = {"op": op, "tokens": tokens, "cols": cols, "experts": experts, "k": k,
+             "pad": rng.choice([1, 16, 128])}
+        if op == "moe_route":
+            c["xq"] = rng.choice(["none", "block", "mx"])
+        return c
+    cols = _size(rng, 64, 16384, 128)
+    rows = min(_size(rng, 1, 16384, 16), max(1, (1 << 26) // cols))
+    c = {"op": op, "rows": rows, "cols": cols}
+    if op.startswith("ln"):
+        c.update(x=rng.choice(["bf16", "f32"]), w=rng.choice(["bf16", "f32"]),
+                 ckpt=rng.random() < 0.5)
+        if op == "ln_fwd":
+            c["yq"] = rng.choice(["none", "tensor", "block", "mx"])
+            c["y"] = c["yq"] == "none" or rng.random() < 0.5
+    elif op.startswith("act"):
+        c.update(act=rng.choice(["gelu", "gelu_tanh", "silu"]), gated=rng.random() < 0.5,
+                 ckpt=rng.random() < 0.7)
+        if op == "act_fwd":
+            c["yq"] = rng.choice(["none", "tensor", "block", "mx"])
+            c["y"] = c["yq"] == "none" or rng.random() < 0.5
+        else:
+            c["y"] = rng.random() < 0.5
+    return c
+
+
+# ----------------------------------------------------------------- inputs
+def _normal(g, *shape):
+    return torch.randn(shape, generator=g, device=DEV, dtype=torch.float32)
+
+
+def _stored(v):
+    """v as an 8-bit checkpoint in hand: E4M3 bytes and the 1x128 tiles' scales."""
+    q, s = _quant_tiles(v, 128, False)
+    return q.view(torch.uint8), s
+
+
+def _sorted(expert, experts, pad, rows):
+    """(offsets, counts, pos, src) of expert ids [tokens][k]: a stable sort by
+    expert, every expert's segment rounded up to a multiple of pad rows."""
+    flat = expert.reshape(-1).long()
+    n = flat.numel()
+    key = torch.where((flat >= 0) & (flat < experts), flat, torch.full_like(flat, experts))
+    counts = (key[:, None] == torch.arange(experts, device=key.device)).sum(0)
+    ends = torch.cumsum((counts + pad - 1) // pad * pad, 0)
+    offsets = torch.cat([ends.new_zeros(1), ends])
+    order = torch.sort(key, stable=True)[1]
+    sorted_key = key[order]
+    starts = torch.cat([counts.new_zeros(1), torch.cumsum(counts, 0)])   # of the unpadded order
+    at = torch.arange(n, device=key.device) - starts[sorted_key] + offsets[sorted_key]
+    kept = sorted_key < experts
+    at = torch.where(kept, at, torch.full_like(at, -1))
+    pos = torch.empty_like(at).scatter_(0, order, at)
+    # dropped entries write to one extra row, cut off again
+    src = torch.full((rows + 1,), -1, dtype=torch.int64, device=key.device)
+    src.scatter_(0, torch.where(kept, at, torch.full_like(at, rows)), order)
+    return (offsets.int(), counts.int(), pos.int().view(expert.shape), src[:rows].int())
+
+
+def _capacity(n, experts, pad):
+    return (n + min(n, experts) * (pad - 1)) // pad * pad
+
+
+def prepare(case, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    s = dict(case)
+    op = case["op"]
+    empty = lambda dt, *shape: torch.empty(shape, dtype=dt, device=DEV)  # noqa: E731
+    if op.startswith("moe"):
+        t, c, e, k = case["tokens"], case["cols"], case["experts"], case["k"]
+        # skewed experts, k different ones a token; a few tokens (a batch's
+        # padding) and a few single choices (over capacity) are dropped
+        load = 0.7 * _normal(g, e)
+        noise = -torch.log(-torch.log(torch.rand((t, e), generator=g, device=DEV) * 0.9998 + 1e-4))
+        score, expert = torch.topk(load + noise, k, dim=1)
+        drop = torch.rand((t, k + 1), generator=g, device=DEV)
+        expert[(drop[:, :1] < 0.02) | (drop[:, 1:] < 0.01)] = -1
+        s["expert"] = expert.int().contiguous()
+        s["weight"] = torch.softmax(score, dim=1).contiguous()
+        r = s["cap"] = _capacity(t * k, e, case["pad"])
+        if op == "moe_route":
+            s["x"] = _normal(g, t, c).bfloat16()
+            s["offsets"], s["counts"] = empty(torch.int32, e + 1), empty(torch.int32, e)
+            s["pos"], s["src"] = empty(torch.int32, t, k), empty(torch.int32, r)
+            # rows past the last segment are not part of the result: they stay zero
+            if case["xq"] == "none":
+                s["xs"] = torch.zeros((r, c), dtype=torch.bfloat16, device=DEV)
+            else:
+                s["q"] = torch.zeros((r, c), dtype=torch.uint8, device=DEV)
+                s["q_s"] = _scale_buffer(case["xq"], r, c).zero_()
+        else:
+            s["offsets"], _, s["pos"], s["src"] = _sorted(s["expert"], e, case["pad"], r)
+            s["ys"] = _normal(g, r, c).bfloat16()
+            if op == "moe_combine":
+                s["y"] = empty(torch.bfloat16, t, c)
+            else:
+                s["dy"] = (1e-3 * _normal(g, t, c)).bfloat16()
+                s["dys"] = torch.zeros((r, c), dtype=torch.bfloat16, device=DEV)
+                s["dw"] = empty(torch.float32, t, k)
+        return s
+    r, c = case["rows"], case["cols"]
+    if op.startswith("ln"):
+        # rows of a residual stream: a few wide channels and a mean of their own
+        wide = torch.where(torch.rand(c, generator=g, device=DEV) < 0.01, 8.0, 1.0)
+        x = ((_normal(g, r, c) + 0.5 * _normal(g, r, 1)) * wide).to(TYPES[case["x"]])
+        w = TYPES[case["w"]]
+        s["gamma"] = (1.0 + 0.2 * _normal(g, c)).to(w)
+        s["beta"] = (0.1 * _normal(g, c)).to(w)
+        s["mean"], s["rstd"] = empty(torch.float32, r), empty(torch.float32, r)
+        if op == "ln_fwd":
+            s["x_in"] = x
+            _output_buffers(s, case, r, c)
+            if case["ckpt"]:
+                s["ck"] = empty(torch.uint8, r, c)
+                s["ck_s"] = empty(torch.float32, r, (c + 127) // 128)
+        else:
+            x32 = x.float()
+            s["mean"] = x32.mean(1)
+            s["rstd"] = 1.0 / torch.sqrt(((x32 - s["mean"][:, None]) ** 2).mean(1) + EPS)
+            if case["ckpt"]:
+                s["ck"], s["ck_s"] = _stored((x32 - s["mean"][:, None]) * s["rstd"][:, None])
+            else:
+                s["x_in"] = x
+            s["dy"] = (1e-3 * _normal(g, r, c)).bfloat16()
+            s["dx"] = empty(TYPES[case["x"]], r, c)
+            s["dgamma"], s["dbeta"] = empty(torch.float32, c), empty(torch.float32, c)
+        return s
+    if op == "ckpt":
+        s["x_in"] = _normal(g, r, c).bfloat16()
+        s["ck"] = empty(torch.uint8, r, c)
+        s["ck_s"] = empty(torch.float32, r, (c + 127) // 128)
+        s["y_out"] = empty(torch.bfloat16, r, c)
+        return s
+    hc = 2 * c if case["gated"] else c
+    h = (1.5 * _normal(g, r, hc)).bfloat16()
+    if op == "act_fwd":
+        s["h"] = h
+        _output_buffers(s, case, r, c)
+        if case["ckpt"]:
+            s["ck"] = empty(torch.uint8, r, hc)
+            s["ck_s"] = empty(torch.float32, r, (hc + 127) // 128)
+    else:
+        if case["ckpt"]:
+            s["ck"], s["ck_s"] = _stored(h.float())
+        else:
+            s["h"] = h
+        s["dy"] = (1e-3 * _normal(g, r, c)).bfloat16()
+        s["dh"] = empty(torch.bfloat16, r, hc)
+        if case["y"]:
+            s["y_out"] = empty(torch.bfloat16, r, c)
+    return s
+
+
+def _scale_buffer(scaling, r, c):
+    if scaling == "block":
+        return torch.empty((r, (c + 127) // 128), dtype=torch.float32, device=DEV)
+    return torch.empty((r, (c + 31) // 32), dtype=torch.uint8, device=DEV)
+
+
+def _output_buffers(s, case, r, c):
+    """The forward passes' output: BF16, and / or an FP8 GEMM operand."""
+    if case["y"]:
+        s["y_out"] = torch.empty((r, c), dtype=torch.bfloat16, device=DEV)
+    if case["yq"] == "tensor":       # delayed scaling: the scale of the steps before
+        s["q"] = torch.empty((r, c), dtype=torch.uint8, device=DEV)
+        s["scale"] = torch.full((1,), 32.0, dtype=torch.float32, device=DEV)
+        s["amax"] = torch.empty(1, dtype=torch.float32, device=DEV)
+    elif case["yq"] != "none":
+        s["q"] = torch.empty((r, c), dtype=torch.uint8, device=DEV)
+        s["q_s"] = _scale_buffer(case["yq"], r, c)
+
+
+# -------------------------------------------------------------- plain form
+def _tiles(v, b):
+    """[rows][cols] -> [rows][tiles][b], the last tile filled up with zeros."""
+    r, c = v.shape
+    n = (c + b - 1) // b
+    return torch.nn.functional.pad(v, (0, n * b - c)).view(r, n, b)
+
+
+def _quant_tiles(v, b, mx):
+    """E4M3 of 32-bit v with one scale per row and b columns: (values, the
+    factors that bring them back, as E8M0 for mx)."""
+    r, c = v.shape
+    t = _tiles(v, b)
+    amax = t.abs().amax(2)
+    if mx:
+        # the smallest e with amax <= 448 * 2^e; 448 = 0.875 * 2^9
+        m, x = torch.frexp(amax)
+        e = torch.where(m <= 0.875, x - 9, x - 8).clamp(-127, 127)
+        e = torch.where(amax == 0, torch.zeros_like(e), e)
+        scale = torch.ldexp(torch.ones_like(amax), -e)
+        back = (e + 127).to(torch.uint8).view(torch.float8_e8m0fnu)
+    else:
+        scale = torch.where((amax > 0) & (amax <= FLT_MAX), (FMAX / amax).clamp(max=FLT_MAX),
+                            torch.ones_like(amax))
+        back = 1.0 / scale
+    q = (t * scale[:, :, None]).clamp(-FMAX, FMAX).view(r, -1)[:, :c]
+    return q.to(torch.float8_e4m3fn).contiguous(), back
+
+
+def _unquant(q, s):
+    """Bytes and 1x128 scales -> 32-bit values."""
+    r, c = q.shape
+    v = q.view(torch.float8_e4m3fn).float()
+    return (_tiles(v, 128) * s[:, :, None]).view(r, -1)[:, :c]
+
+
+def _act32(name, h):
+    """(act(h), act'(h)) in h's precision."""
+    if name == "silu":
+        p = 1.0 / (1.0 + torch.exp(-h))
+        return h * p, p * (1.0 + h * (1.0 - p))
+    if name == "gelu":
+        p = 0.5 * torch.special.erfc(h * -math.sqrt(0.5))
+        return h * p, p + h * torch.exp(-0.5 * h * h) * (1.0 / math.sqrt(2.0 * math.pi))
+    a = math.sqrt(2.0 / math.pi)
+    # 0.5 (1 + tanh u) = 1 / (1 + exp(-2u))
+    p = 1.0 / (1.0 + torch.exp(-2.0 * a * (h + 0.044715 * h * h * h)))
+    return h * p, p + 2.0 * a * h * p * (1.0 - p) * (1.0 + 3.0 * 0.044715 * h * h)
+
+
+def _plain_operand(out, case, y):
+    """The requested forms of the 32-bit result y."""
+    if case["y"]:
+        out["y"] = y.bfloat16()
+    if case["yq"] == "tensor":
+        out["q"] = (y * 32.0).clamp(-FMAX, FMAX).to(torch.float8_e4m3fn)
+        out["amax"] = y.abs().amax().view(1)
+    elif case["yq"] != "none":
+        mx = case["yq"] == "mx"
+        out["q"], out["q_scale"] = _quant_tiles(y, 32 if mx else 128, mx)
+
+
+def _plain(s):
+    op, out = s["op"], {}
+    if op == "ln_fwd":
+        x = s["x_in"].float()
+        mean = x.mean(1)
+        d = x - mean[:, None]
+        rstd = 1.0 / torch.sqrt((d * d).mean(1) + EPS)
+        xhat = d * rstd[:, None]
+        out["mean"], out["rstd"] = mean, rstd
+        _plain_operand(out, s, xhat * s["gamma"].float() + s["beta"].float())
+        if s["ckpt"]:
+            out["ck"], out["ck_scale"] = _quant_tiles(xhat, 128, False)
+    elif op == "ln_bwd":
+        rstd = s["rstd"][:, None]
+        xhat = (_unquant(s["ck"], s["ck_s"]) if s["ckpt"]
+                else (s["x_in"].float() - s["mean"][:, None]) * rstd)
+        dy = s["dy"].float()
+        g = dy * s["gamma"].float()
+        dx = rstd * (g - g.mean(1, keepdim=True) - xhat * (g * xhat).mean(1, keepdim=True))
+        out["dx"] = dx.to(TYPES[s["x"]])
+        out["dgamma"], out["dbeta"] = (dy * xhat).sum(0), dy.sum(0)
+    elif op == "act_fwd":
+        h, c = s["h"].float(), s["cols"]
+        a = _act32(s["act"], h[:, :c])[0]
+        _plain_operand(out, s, a * h[:, c:] if s["gated"] else a)
+        if s["ckpt"]:
+            out["ck"], out["ck_scale"] = _quant_tiles(h, 128, False)
+    elif op == "act_bwd":
+        h, c = _unquant(s["ck"], s["ck_s"]) if s["ckpt"] else s["h"].float(), s["cols"]
+        dy = s["dy"].float()
+        a, da = _act32(s["act"], h[:, :c])
+        if s["gated"]:
+            out["dh"] = torch.cat([dy * h[:, c:] * da, dy * a], 1).bfloat16()
+        else:
+            out["dh"] = (dy * da).bfloat16()
+        if s["y"]:
+            out["y"] = (a * h[:, c:] if s["gated"] else a).bfloat16()
+    elif op == "ckpt":
+        out["ck"], out["ck_scale"] = _quant_tiles(s["x_in"].float(), 128, False)
+        out["y"] = _unquant(out["ck"], out["ck_scale"]).bfloat16()
+    elif op == "moe_route":
+        out["offsets"], out["counts"], out["pos"], src = _sorted(s["expert"], s["experts"],
+                                                                 s["pad"], s["cap"])
+        out["src"] = src
+        real = src >= 0
+        xs = s["x"][torch.where(real, src, torch.zeros_like(src)).long() // s["k"]]
+        xs = xs * real[:, None]
+        if s["xq"] == "none":
+            out["xs"] = xs
+        else:
+            mx = s["xq"] == "mx"
+            out["q"], scale = _quant_tiles(xs.float(), 32 if mx else 128, mx)
+            # rows past the last segment hold nothing, not even a scale
+            inside = torch.arange(s["cap"], device=src.device) < out["offsets"][-1]
+            out["q_scale"] = ((scale.view(torch.uint8) * inside[:, None]).view(scale.dtype)
+                              if mx else scale * inside[:, None])
+    elif op == "moe_combine":
+        kept = s["pos"] >= 0
+        rows = s["ys"].float()[torch.where(kept, s["pos"], torch.zeros_like(s["pos"])).long()]
+        out["y"] = (rows * (s["weight"] * kept)[:, :, None]).sum(1).bfloat16()
+    else:
+        real = s["src"] >= 0
+        at = torch.where(real, s["src"], torch.zeros_like(s["src"])).long()
+        d = s["dy"].float()[at // s["k"]]
+        out["dys"] = (d * (s["weight"].reshape(-1)[at] * real)[:, None]).bfloat16()
+        dot = (d * s["ys"].float()).sum(1)
+        kept = s["pos"] >= 0
+        out["dw"] = dot[torch.where(kept, s["pos"], torch.zeros_like(s["pos"])).long()] * kept
+    return out
+
+
+# -------------------------------------------------------- the framework's
+def _scaling(F, name):
+    return {"tensor": F.SCALE_TENSOR, "block": F.SCALE_BLOCK_1x128, "mx": F.SCALE_MX_1x32}[name]
+
+
+def _cast(F, s):
+    if s["yq"] == "none":
+        return None
+    return F.cast_out(s["q"], F.E4M3, _scaling(F, s["yq"]), s.get("q_s"), s.get("scale"),
+                      s.get("amax"))
+
+
+def _held(s, out, scaling):
+    """The FP8 operand's buffers as the values that they stand for."""
+    if scaling == "none":
+        return
+    out["q"] = s["q"].view(torch.float8_e4m3fn)
+    if scaling == "tensor":
+        out["amax"] = s["amax"]
+    else:
+        out["q_scale"] = s["q_s"].view(torch.float8_e8m0fnu) if scaling == "mx" else s["q_s"]
+
+
+def _framework(s):
+    from scaled_fp8_gemm_amd import fp8sg as F
+    op, out = s["op"], {}
+    act = {"gelu": 0, "gelu_tanh": 1, "silu": 2}.get(s.get("act"))
+    if op == "ln_fwd":
+        ck = (F.cast_out(s["ck"], F.E4M3, F.SCALE_BLOCK_1x128, s["ck_s"]) if s["ckpt"] else None)
+        if s["yq"] == "tensor" and "ws" not in s:
+            s["ws"] = F.workspace()
+        F.fp8_layernorm_fwd(s["x_in"], s["gamma"], s["beta"], EPS, s.get("y_out"), s["mean"],
+                            s["rstd"], yq=_cast(F, s), xhat=ck, workspace=s.get("ws"))
+        out["mean"], out["rstd"] = s["mean"], s["rstd"]
+    elif op == "ln_bwd":
+        if "ws" not in s:
+            s["ws"] = F.layernorm_workspace(s["rows"], s["cols"])
+        ck = (F.operand(s["ck"], F.E4M3, F.SCALE_BLOCK_1x128, s["ck_s"]) if s["ckpt"] else None)
+        F.fp8_layernorm_bwd(s["dy"], None if s["ckpt"] else s["x_in"],
+                            None if s["ckpt"] else s["mean"], s["rstd"], s["gamma"], s["dx"],
+                            s["dgamma"], s["dbeta"], xhat=ck, workspace=s["ws"])
+        return {"dx": s["dx"], "dgamma": s["dgamma"], "dbeta": s["dbeta"]}
+    elif op == "act_fwd":
+        ck = (F.cast_out(s["ck"], F.E4M3, F.SCALE_BLOCK_1x128, s["ck_s"]) if s["ckpt"] else None)
+        if s["yq"] == "tensor" and "ws" not in s:
+            s["ws"] = F.workspace()
+        F.fp8_act_fwd(s["h"], act, s["gated"], s.get("y_out"), yq=_cast(F, s), ckpt=ck,
+                      workspace=s.get("ws"))
+    elif op == "act_bwd":
+        h = (F.operand(s["ck"], F.E4M3, F.SCALE_BLOCK_1x128, s["ck_s"]) if s["ckpt"] else s["h"])
+        F.fp8_act_bwd(s["dy"], h, act, s["gated"], s["dh"], y=s.get("y_out"))
+        out["dh"] = s["dh"]
+        if s["y"]:
+            out["y"] = s["y_out"]
+        return out
+    elif op == "ckpt":
+        F.fp8_checkpoint_save(s["x_in"], F.cast_out(s["ck"], F.E4M3, F.SCALE_BLOCK_1x128,
+                                                    s["ck_s"]))
+        F.fp8_checkpoint_load(F.operand(s["ck"], F.E4M3, F.SCALE_BLOCK_1x128, s["ck_s"]),
+                              s["rows"], s["cols"], s["y_out"])
+        return {"ck": s["ck"].view(torch.float8_e4m3fn), "ck_scale": s["ck_s"], "y": s["y_out"]}
+    elif op == "moe_route":
+        if "ws" not in s:
+            s["ws"] = F.moe_workspace(s["tokens"] * s["k"], s["experts"])
+        F.fp8_moe_sort(s["expert"], s["experts"], s["pad"], s["offsets"], s["counts"], s["pos"],
+                       s["src"], workspace=s["ws"])
+        xq = (None if s["xq"] == "none"
+              else F.cast_out(s["q"], F.E4M3, _scaling(F, s["xq"]), s["q_s"]))
+        F.fp8_moe_dispatch(s["x"], s["pos"], s["src"], s["offsets"], s.get("xs"), xq=xq)
+        out = {k: s[k] for k in ("offsets", "counts", "pos", "src")}
+        if s["xq"] == "none":
+            out["xs"] = s["xs"]
+        _held(s, out, s["xq"])
+        return out
+    elif op == "moe_combine":
+        F.fp8_moe_combine(s["ys"], s["pos"], s["weight"], s["y"])
+        return {"y": s["y"]}
+    else:
+        F.fp8_moe_combine_bwd(s["dy"], s["ys"], s["weight"], s["pos"], s["src"], s["offsets"],
+                              s["dys"], s["dw"])
+        return {"dys": s["dys"], "dw": s["dw"]}
+    if s["y"]:
+        out["y"] = s["y_out"]
+    _held(s, out, s["yq"])
+    if s["ckpt"]:
+        out["ck"], out["ck_scale"] = s["ck"].view(torch.float8_e4m3fn), s["ck_s"]
+    return out
+
+
+def run(state):
+    return _framework(state) if own else _plain(state)
+
+
+# ------------------------------------------------------------- in 64 bits
+def _exact_cast(v, b, mx):
+    """(v / factor, factor) without rounding: the values that the bytes and
+    scales of an E4M3 cast with b-column blocks approximate."""
+    r, c = v.shape
+    n = -(-c // b)
+    big = v.abs().new_zeros((r, n * b))
+    big[:, :c] = v.abs()
+    big = big.view(r, n, b).amax(2)
+    if mx:
+        factor = torch.exp2(torch.ceil(torch.log2(big / FMAX)))
+        # log2 may land an ulp off at a power of two: settle it by comparing
+        factor = torch.where(big > FMAX * factor, 2 * factor, factor)
+        factor = torch.where(big <= FMAX * factor / 2, factor / 2, factor)
+    else:
+        factor = big / FMAX
+    factor = torch.where(big == 0, torch.ones_like(big), factor)
+    return v / factor.repeat_interleave(b, 1)[:, :c], factor
+
+
+def _exact_act(name, h):
+    if name == "silu":
+        p = torch.sigmoid(h)
+        return h * p, p + h * p * (1 - p)
+    if name == "gelu":
+        p = torch.special.ndtr(h)
+        return h * p, p + h * torch.exp(-h * h / 2) / math.sqrt(2 * math.pi)
+    u = math.sqrt(2 / math.pi) * (h + 0.044715 * h ** 3)
+    t = torch.tanh(u)
+    slope = math.sqrt(2 / math.pi) * (1 + 0.134145 * h ** 2)
+    return 0.5 * h * (1 + t), 0.5 * (1 + t) + 0.5 * h * (1 - t * t) * slope
+
+
+def _exact_forms(out, case, y):
+    if case["y"]:
+        out["y"] = y
+    if case["yq"] == "tensor":
+        out["q"], out["amax"] = (32 * y).clamp(-FMAX, FMAX), y.abs().max().view(1)
+    elif case["yq"] != "none":
+        mx = case["yq"] == "mx"
+        out["q"], out["q_scale"] = _exact_cast(y, 32 if mx else 128, mx)
+
+
+def _exact_held(s):
+    """The stored checkpoint's values."""
+    v = s["ck"].view(torch.float8_e4m3fn).double()
+    return v * s["ck_s"].double().repeat_interleave(128, 1)[:, :v.shape[1]]
+
+
+def _exact_sort(expert, experts, pad, rows):
+    e = expert.cpu().numpy().reshape(-1)
+    counts = np.array([(e == i).sum() for i in range(experts)])
+    offsets = np.concatenate([[0], np.cumsum(-(-counts // pad) * pad)])
+    pos, src = np.full(e.size, -1), np.full(rows, -1)
+    for i in range(experts):
+        where = np.flatnonzero(e == i)
+        pos[where] = offsets[i] + np.arange(where.size)
+        src[pos[where]] = where
+    return [torch.from_numpy(v.astype(np.int32)) for v in (offsets, counts,
+                                                           pos.reshape(expert.shape), src)]
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op, out = case["op"], {}
+    if op.startswith("moe"):
+        t, k, c = case["tokens"], case["k"], case["cols"]
+        offsets, counts, pos, src = _exact_sort(s["expert"], case["experts"], case["pad"],
+                                                s["cap"])
+        pos, src = pos.to(DEV).long(), src.to(DEV).long()
+        if op == "moe_route":
+            out.update(offsets=offsets, counts=counts, pos=pos.int(), src=src.int())
+            xs = torch.zeros((s["cap"], c), dtype=torch.float64, device=DEV)
+            xs[src >= 0] = s["x"].double()[src[src >= 0] // k]
+            if case["xq"] == "none":
+                out["xs"] = xs
+            else:
+                mx = case["xq"] == "mx"
+                out["q"], factor = _exact_cast(xs, 32 if mx else 128, mx)
+                end = int(offsets[-1])
+                factor[end:] = 2.0 ** -127 if mx else 0.0   # the E8M0 byte 0
+                out["q_scale"] = factor
+        elif op == "moe_combine":
+            y = torch.zeros((t, c), dtype=torch.float64, device=DEV)
+            for j in range(k):
+                at = pos[:, j]
+                y[at >= 0] += s["weight"][at >= 0, j, None].double() * s["ys"][at[at >= 0]].double()
+            out["y"] = y
+        else:
+            dys = torch.zeros((s["cap"], c), dtype=torch.float64, device=DEV)
+            dw = torch.zeros((t, k), dtype=torch.float64, device=DEV)
+            for j in range(k):
+                ok = pos[:, j] >= 0
+                at, dy = pos[ok, j], s["dy"][ok].double()
+                dys[at] = s["weight"][ok, j, None].double() * dy
+                dw[ok, j] = (dy * s["ys"][at].double()).sum(1)
+            out["dys"], out["dw"] = dys, dw
+        return out
+    if op == "ln_fwd":
+        x = s["x_in"].double()
+        var, mean = torch.var_mean(x, 1, correction=0)
+        out["mean"], out["rstd"] = mean, (var + EPS).rsqrt()
+        xhat = (x - mean[:, None]) * out["rstd"][:, None]
+        _exact_forms(out, case, xhat * s["gamma"].double() + s["beta"].double())
+        if case["ckpt"]:
+            out["ck"], out["ck_scale"] = _exact_cast(xhat, 128, False)
+    elif op == "ln_bwd":
+        rstd, dy = s["rstd"].double()[:, None], s["dy"].double()
+        xhat = _exact_held(s) if case["ckpt"] else (s["x_in"].double()
+                                                    - s["mean"].double()[:, None]) * rstd
+        n = case["cols"]
+        g = dy * s["gamma"].double()
+        out["dx"] = rstd / n * (n * g - g.sum(1, True) - xhat * (g * xhat).sum(1, True))
+        out["dgamma"], out["dbeta"] = (dy * xhat).sum(0), dy.sum(0)
+    elif op == "ckpt":
+        x = s["x_in"].double()
+        out["ck"], out["ck_scale"] = _exact_cast(x, 128, False)
+        out["y"] = None              # differs from x by the 8-bit rounding, which it is to show
+    else:
+        c = case["cols"]
+        h = _exact_held(s) if op == "act_bwd" and case["ckpt"] else s["h"].double()
+        a, da = _exact_act(case["act"], h[:, :c])
+        y = a * h[:, c:] if case["gated"] else a
+        if op == "act_fwd":
+            _exact_forms(out, case, y)
+            if case["ckpt"]:
+                out["ck"], out["ck_scale"] = _exact_cast(h, 128, False)
+        else:
+            dy = s["dy"].double()
+            out["dh"] = (torch.cat([dy * h[:, c:] * da, dy * a], 1) if case["gated"] else dy * da)
+            if case["y"]:
+                out["y"] = y
+    return out
+
+
+# -------------------------------------------------------------------- work
+def _operand_bytes(scaling, r, c):
+    if scaling == "none":
+        return 0
+    return r * c + {"tensor": 8, "block": 4 * r * -(-c // 128), "mx": r * -(-c // 32)}[scaling]
+
+
+def work(case):
+    op = case["op"]
+    if op.startswith("moe"):
+        t, c, k, e = case["tokens"], case["cols"], case["k"], case["experts"]
+        n, r = t * k, _capacity(t * k, e, case["pad"])
+        if op == "moe_route":
+            row = (2 * n * c if case["xq"] == "none" else _operand_bytes(case["xq"], n, c))
+            return {"bytes": 2 * t * c + row + 4 * (2 * n + r + 2 * e + 1), "flops": n * c}
+        if op == "moe_combine":
+            return {"bytes": 2 * n * c + 2 * t * c + 8 * n, "flops": 2 * n * c}
+        return {"bytes": 2 * t * c + 4 * n * c + 12 * n, "flops": 3 * n * c}
+    r, c = case["rows"], case["cols"]
+    n = r * c
+    if op.startswith("ln"):
+        xb, wb = {"bf16": 2, "f32": 4}[case["x"]], {"bf16": 2, "f32": 4}[case["w"]]
+        held = _operand_bytes("block", r, c) if case["ckpt"] else 0
+        if op == "ln_fwd":
+            return {"bytes": xb * n + (2 * n if case["y"] else 0) + held
+                    + _operand_bytes(case["yq"], r, c) + 8 * r + 2 * wb * c, "flops": 8 * n}
+        return {"bytes": 2 * n + (held or xb * n + 4 * r) + xb * n + 4 * r + wb * c + 8 * c,
+                "flops": 14 * n}
+    if op == "ckpt":
+        return {"bytes": 2 * n + 2 * _operand_bytes("block", r, c) + 2 * n, "flops": 4 * n}
+    hc = 2 * c if case["gated"] else c
+    held = _operand_bytes("block", r, hc) if case["ckpt"] else 0
+    if op == "act_fwd":
+        return {"bytes": 2 * r * hc + (2 * n if case["y"] else 0) + held
+                + _operand_bytes(case["yq"], r, c), "flops": 12 * n}
+    return {"bytes": 2 * n + (held or 2 * r * hc) + 2 * r * hc + (2 * n if case["y"] else 0),
+            "flops": 24 * n}
