@@ -227,11 +227,13 @@ def prepare(case, seed):
         s["h"] = h
         _output_buffers(s, case, r, c)
         if case["ckpt"]:
+            # the gate and up halves of a row have tiles of their own
             s["ck"] = empty(torch.uint8, r, hc)
-            s["ck_s"] = empty(torch.float32, r, (hc + 127) // 128)
+            s["ck_s"] = empty(torch.float32, r * hc // c, (c + 127) // 128)
     else:
         if case["ckpt"]:
-            s["ck"], s["ck_s"] = _stored(h.float())
+            s["ck"], s["ck_s"] = _stored(h.float().view(-1, c))
+            s["ck"] = s["ck"].view(r, hc)
         else:
             s["h"] = h
         s["dy"] = (1e-3 * _normal(g, r, c)).bfloat16()
@@ -348,10 +350,12 @@ def _plain(s):
         a = _act32(s["act"], h[:, :c])[0]
         _plain_operand(out, s, a * h[:, c:] if s["gated"] else a)
         if s["ckpt"]:
-            out["ck"], out["ck_scale"] = _quant_tiles(h, 128, False)
+            out["ck"], out["ck_scale"] = _quant_tiles(h.view(-1, c), 128, False)
+            out["ck"] = out["ck"].view(h.shape)
     elif op == "act_bwd":
-        h, c = _unquant(s["ck"], s["ck_s"]) if s["ckpt"] else s["h"].float(), s["cols"]
-        dy = s["dy"].float()
+        dy, c = s["dy"].float(), s["cols"]
+        h = (_unquant(s["ck"].view(-1, c), s["ck_s"]).reshape(s["ck"].shape) if s["ckpt"]
+             else s["h"].float())
         a, da = _act32(s["act"], h[:, :c])
         if s["gated"]:
             out["dh"] = torch.cat([dy * h[:, c:] * da, dy * a], 1).bfloat16()
@@ -531,8 +535,9 @@ def _exact_forms(out, case, y):
 
 def _exact_held(s):
     """The stored checkpoint's values."""
-    v = s["ck"].view(torch.float8_e4m3fn).double()
-    return v * s["ck_s"].double().repeat_interleave(128, 1)[:, :v.shape[1]]
+    v = s["ck"].view(torch.float8_e4m3fn).double().view(-1, s["cols"])
+    v = v * s["ck_s"].double().repeat_interleave(128, 1)[:, :v.shape[1]]
+    return v.view(s["ck"].shape)
 
 
 def _exact_sort(expert, experts, pad, rows):
@@ -612,7 +617,8 @@ def exact(case, seed):
         if op == "act_fwd":
             _exact_forms(out, case, y)
             if case["ckpt"]:
-                out["ck"], out["ck_scale"] = _exact_cast(h, 128, False)
+                out["ck"], out["ck_scale"] = _exact_cast(h.view(-1, c), 128, False)
+                out["ck"] = out["ck"].view(h.shape)
         else:
             dy = s["dy"].double()
             out["dh"] = (torch.cat([dy * h[:, c:] * da, dy * a], 1) if case["gated"] else dy * da)
@@ -652,7 +658,7 @@ def work(case):
     if op == "ckpt":
         return {"bytes": 2 * n + 2 * _operand_bytes("block", r, c) + 2 * n, "flops": 4 * n}
     hc = 2 * c if case["gated"] else c
-    held = _operand_bytes("block", r, hc) if case["ckpt"] else 0
+    held = _operand_bytes("block", r * hc // c, c) if case["ckpt"] else 0
     if op == "act_fwd":
         return {"bytes": 2 * r * hc + (2 * n if case["y"] else 0) + held
                 + _operand_bytes(case["yq"], r, c), "flops": 12 * n}
