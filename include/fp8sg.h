@@ -24,7 +24,8 @@
  *               allocates nothing and keeps no state between calls.
  *   Workspace   The calls that produce an amax (fp8_amax*, fp8_quantize_tensor*
  *               with amax_out, fp8_quantize_tensor_current,
- *               fp8_quantize_pair_current, fp8_gemm_fprop_fused with y_amax)
+ *               fp8_quantize_pair_current, fp8_gemm_fprop_fused with y_amax,
+ *               fp8_layernorm_fwd and fp8_act_fwd with an amax)
  *               reduce through a caller-owned device workspace of
  *               FP8_WORKSPACE_BYTES, 256-byte aligned: partial maxima, and
  *               the counters and flags of the one-launch grid-wide maximum.
@@ -54,7 +55,10 @@
  *               a failing check returns its status and has no side effect.
  *               FP8_ERR_HIP reports a launch failure.  NaN/inf data are not
  *               errors; they follow the rules above.
- *   Alignment   Data pointers must be 16-byte aligned (FP8_ERR_ALIGN).
+ *   Alignment   Data pointers must be 16-byte aligned (FP8_ERR_ALIGN).  The
+ *               row operators (layer norm, activations, checkpoints, expert
+ *               sorting) take rows of any length; their short last tile of
+ *               a row has a scale of its own.
  *   Empty       A tensor with zero elements may be passed as NULL; required
  *               pointers to non-empty tensors and to outputs such as amax may
  *               not (FP8_ERR_NULL).
@@ -378,6 +382,185 @@ fp8_status_t fp8_gemm_wgrad_f32(const fp8_operand_t* dyT, const fp8_operand_t* x
  * routine; this entry point lets that routine be checked on any FP32 input.
  *   x  in float[n];  q  out uint8[n].  Errors: NULL; n < 0; alignment; fmt. */
 fp8_status_t fp8_convert_f32(const float* x, int64_t n, int32_t fmt, uint8_t* q, void* stream);
+
+/* ---- Row operators: what a training step computes between its GEMMs ----
+ *
+ * An output of a row operator cast to FP8, as the next GEMM's operand or as
+ * an 8-bit checkpoint for the backward pass.  The cast takes the 32-bit
+ * result (not its BF16 rounding) under the rules above.
+ *   FP8_SCALE_TENSOR      scale in float[1] (delayed scaling); amax out
+ *                         float[1], nullable: the largest magnitude of the
+ *                         32-bit results
+ *   FP8_SCALE_BLOCK_1x128 scale_inv out float [rows][ceil(cols/128)]
+ *   FP8_SCALE_MX_1x32     scale_inv out uint8 E8M0 [rows][ceil(cols/32)]
+ * data: out uint8 [rows][cols].  Fields that a scaling does not use are
+ * ignored. */
+typedef struct {
+  uint8_t* data;
+  int32_t fmt;             /* fp8_format_t  */
+  int32_t scaling;         /* fp8_scaling_t */
+  void* scale_inv;
+  const float* scale;
+  float* amax;
+} fp8_cast_out_t;
+
+typedef enum { FP8_TYPE_BF16 = 0, FP8_TYPE_F32 = 1 } fp8_type_t;
+
+typedef enum {
+  FP8_ACT_GELU = 0,        /* h Phi(h)                                          */
+  FP8_ACT_GELU_TANH = 1,   /* 0.5 h (1 + tanh(sqrt(2/pi) (h + 0.044715 h^3)))   */
+  FP8_ACT_SILU = 2         /* h / (1 + e^-h)                                    */
+} fp8_act_t;
+
+/* Layer norm.  mean = sum_j x_j / cols, rstd = 1 / sqrt(sum_j (x_j - mean)^2
+ * / cols + eps), xhat = (x - mean) rstd, y = xhat gamma + beta, in FP32.
+ *   x            [rows][cols] of x_type (fp8_type_t), 1 <= cols <= 32768
+ *   gamma, beta  [cols] of w_type (fp8_type_t)
+ *   y_bf16       out [rows][cols] BF16, nullable
+ *   mean, rstd   out float[rows] each
+ *   yq           y cast to FP8, nullable (not FP8_SCALE_BLOCK_128x128)
+ *   xhat         the normalised rows as a checkpoint for fp8_layernorm_bwd,
+ *                nullable (FP8_SCALE_BLOCK_1x128)
+ *   workspace    see Workspace; needed where yq has an amax, else may be NULL
+ * At least one of y_bf16, yq and xhat must be given (FP8_ERR_NULL).
+ * Errors: NULL; enums and scalings; sizes; eps not a finite number >= 0
+ * (FP8_ERR_SHAPE); alignment. */
+fp8_status_t fp8_layernorm_fwd(const void* x, int32_t x_type, const void* gamma, const void* beta,
+                               int32_t w_type, int64_t rows, int64_t cols, float eps,
+                               void* y_bf16, float* mean, float* rstd, const fp8_cast_out_t* yq,
+                               const fp8_cast_out_t* xhat, void* workspace, void* stream);
+
+/* Bytes of fp8_layernorm_bwd's workspace (one row of 2 cols floats for each
+ * of its workgroups; 0 for rows = 0 or sizes that the call rejects). */
+int64_t fp8_layernorm_workspace_bytes(int64_t rows, int64_t cols);
+
+/* Layer norm's gradients, with g = dy gamma:
+ *   dx = rstd (g - mean_j(g) - xhat mean_j(g xhat))
+ *   dgamma = sum over rows of dy xhat,  dbeta = sum over rows of dy
+ * in FP32; the sums over rows have an order of their own for each size, so
+ * that equal calls give equal bits.
+ *   dy_bf16      [rows][cols] BF16
+ *   x, mean      as in the forward pass; both NULL with xhat
+ *   xhat         the checkpoint of the normalised rows instead of x:
+ *                FP8_SCALE_BLOCK_1x128, scales [rows][ceil(cols/128)]; NULL
+ *                with x
+ *   rstd         float[rows]
+ *   dx           out [rows][cols] of x_type
+ *   dgamma, dbeta   out float[cols] each (zeros for rows = 0)
+ *   workspace    fp8_layernorm_workspace_bytes, 256-byte aligned, any
+ *                contents (not the amax workspace); not shared by calls that
+ *                may run at the same time
+ * Errors: NULL; neither or both of x and xhat (FP8_ERR_NULL); enums;
+ * sizes; alignment. */
+fp8_status_t fp8_layernorm_bwd(const void* dy_bf16, const void* x, int32_t x_type,
+                               const float* mean, const float* rstd, const fp8_operand_t* xhat,
+                               const void* gamma, int32_t w_type, int64_t rows, int64_t cols,
+                               void* dx, float* dgamma, float* dbeta, void* workspace,
+                               void* stream);
+
+/* An activation between two GEMMs: y = act(h), or with gated = 1, where a
+ * row of h is [a | u], y = act(a) u.
+ *   h_bf16   [rows][cols] BF16, gated [rows][2 cols]
+ *   y_bf16   out [rows][cols] BF16, nullable
+ *   yq       y cast to FP8, nullable (not FP8_SCALE_BLOCK_128x128)
+ *   ckpt     h as a checkpoint for fp8_act_bwd, nullable
+ *            (FP8_SCALE_BLOCK_1x128): bytes as h, scales
+ *            [rows * (1 + gated)][ceil(cols/128)] (the halves of a gated row
+ *            have tiles of their own)
+ *   workspace   see Workspace; needed where yq has an amax, else may be NULL
+ * At least one output must be given (FP8_ERR_NULL).
+ * Errors: NULL; enums, gated not 0 or 1, scalings; sizes; alignment. */
+fp8_status_t fp8_act_fwd(const void* h_bf16, int32_t act, int32_t gated, int64_t rows,
+                         int64_t cols, void* y_bf16, const fp8_cast_out_t* yq,
+                         const fp8_cast_out_t* ckpt, void* workspace, void* stream);
+
+/* The activation's gradient: dh = dy act'(h), or [dy u act'(a) | dy act(a)].
+ *   dy_bf16  [rows][cols] BF16
+ *   h_bf16   the forward pass's input, NULL with ckpt
+ *   ckpt     its checkpoint, as fp8_act_fwd writes it, NULL with h_bf16
+ *   dh_bf16  out, laid out as h
+ *   y_bf16   out [rows][cols] BF16, nullable: y again, from what h was read
+ *            as, for the next weight gradient
+ * Errors: NULL; neither or both of h_bf16 and ckpt (FP8_ERR_NULL); enums;
+ * sizes; alignment. */
+fp8_status_t fp8_act_bwd(const void* dy_bf16, const void* h_bf16, const fp8_operand_t* ckpt,
+                         int32_t act, int32_t gated, int64_t rows, int64_t cols, void* dh_bf16,
+                         void* y_bf16, void* stream);
+
+/* A BF16 activation kept in 8 bits and brought back: fp8_quantize_block's
+ * 1x128 cast for rows of any length, and BF16(bytes * scale_inv).
+ *   x_bf16 / y_bf16   [rows][cols] BF16
+ *   ckpt              FP8_SCALE_BLOCK_1x128
+ * Errors: NULL; enums; sizes; alignment. */
+fp8_status_t fp8_checkpoint_save(const void* x_bf16, int64_t rows, int64_t cols,
+                                 const fp8_cast_out_t* ckpt, void* stream);
+fp8_status_t fp8_checkpoint_load(const fp8_operand_t* ckpt, int64_t rows, int64_t cols,
+                                 void* y_bf16, void* stream);
+
+/* Rows that hold any sort of n choices among `experts` experts with segments
+ * rounded up to `pad`: (n + min(n, experts) (pad - 1)) / pad * pad.  And the
+ * bytes of fp8_moe_sort's workspace.  0 for sizes that the call rejects. */
+int64_t fp8_moe_rows(int64_t n, int32_t experts, int32_t pad);
+int64_t fp8_moe_workspace_bytes(int64_t n, int32_t experts);
+
+/* The tokens' choices sorted by expert, stable: choice i = token * k + j of
+ * n = tokens k is sent to row pos[i] = offsets[e] + the number of choices
+ * before i of the same expert e.
+ *   expert    int32 [tokens][k]; ids outside [0, experts) are dropped
+ *   experts   1 .. 1024
+ *   pad       >= 1: every expert's segment is rounded up to a multiple (128
+ *             for the blockwise GEMMs, 16 for the others)
+ *   rows      rows of src, at least fp8_moe_rows(n, experts, pad)
+ *   offsets   out int32 [experts + 1]: segment starts, and the rows in use
+ *   counts    out int32 [experts]: choices of each expert
+ *   pos       out int32 [tokens][k]; -1 for a dropped choice
+ *   src       out int32 [rows]: the choice in each row; -1 in padding and
+ *             past the last segment
+ *   workspace fp8_moe_workspace_bytes, 4-byte aligned, any contents; not
+ *             shared by calls that may run at the same time
+ * Errors: NULL; sizes (FP8_ERR_SHAPE; rows must be under 2^31); alignment. */
+fp8_status_t fp8_moe_sort(const int32_t* expert, int64_t tokens, int32_t k, int32_t experts,
+                          int32_t pad, int64_t rows, int32_t* offsets, int32_t* counts,
+                          int32_t* pos, int32_t* src, void* workspace, void* stream);
+
+/* Token rows to their experts: row pos[t][j] = x[t], as BF16 and / or cast
+ * to FP8; padding rows inside segments get zeros (their scales 1); rows past
+ * the last segment are left alone.
+ *   x_bf16    [tokens][cols] BF16
+ *   pos, src, offsets   from fp8_moe_sort (a pos outside [0, rows) counts as
+ *             dropped)
+ *   xs_bf16   out [rows][cols] BF16, nullable
+ *   xq        out, nullable (not FP8_SCALE_BLOCK_128x128; no amax: that of
+ *             x is fp8_amax's)
+ * Errors: NULL; enums; sizes; alignment. */
+fp8_status_t fp8_moe_dispatch(const void* x_bf16, int64_t tokens, int32_t k, int64_t cols,
+                              const int32_t* pos, const int32_t* src, const int32_t* offsets,
+                              int32_t experts, int64_t rows, void* xs_bf16,
+                              const fp8_cast_out_t* xq, void* stream);
+
+/* The experts' outputs back: y[t] = sum_j weight[t][j] ys[pos[t][j]], summed
+ * in FP32 in the order of j; dropped choices add nothing, whatever their
+ * weight.  With weight = NULL (all 1) it is fp8_moe_dispatch's gradient.
+ *   ys_bf16   [rows][cols] BF16;  pos  [tokens][k]
+ *   weight    float [tokens][k], nullable
+ *   y_bf16    out [tokens][cols] BF16
+ * Errors: NULL; sizes; alignment. */
+fp8_status_t fp8_moe_combine(const void* ys_bf16, const int32_t* pos, const float* weight,
+                             int64_t tokens, int32_t k, int64_t cols, int64_t rows, void* y_bf16,
+                             void* stream);
+
+/* Its gradient: dys[pos[t][j]] = weight[t][j] dy[t], zeros in padding rows
+ * inside segments (rows past the last segment are left alone), and
+ * dweight[t][j] = dy[t] . ys[pos[t][j]] in FP32, 0 for dropped choices.
+ *   dy_bf16   [tokens][cols] BF16;  ys_bf16  [rows][cols] BF16
+ *   weight    float [tokens][k];  pos, src, offsets  from fp8_moe_sort
+ *   dys_bf16  out [rows][cols] BF16 (not ys_bf16)
+ *   dweight   out float [tokens][k]
+ * Errors: NULL; sizes; alignment. */
+fp8_status_t fp8_moe_combine_bwd(const void* dy_bf16, const void* ys_bf16, const float* weight,
+                                 const int32_t* pos, const int32_t* src, const int32_t* offsets,
+                                 int64_t tokens, int32_t k, int64_t cols, int32_t experts,
+                                 int64_t rows, void* dys_bf16, float* dweight, void* stream);
 
 /* Text for a status code (static storage). */
 const char* fp8_status_string(fp8_status_t status);

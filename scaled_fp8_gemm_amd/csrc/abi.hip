@@ -151,6 +151,68 @@ fp8_status_t quantize_tensor_any(const void* x, int64_t rows, int64_t cols, int3
                                            amax_out ? wsp(ws) : nullptr, st(stream), in));
 }
 
+// A row operator's FP8 output of n elements: any scaling but 128x128, only
+// 1x128 as a checkpoint; amax_ok: a tensor-scaled one may ask for its amax.
+using fp8sg::CastOut;
+fp8_status_t cast_out_ok(const fp8_cast_out_t* o, bool checkpoint, bool amax_ok, int64_t n) {
+  if (!o) return FP8_OK;
+  if (!fmt_ok(o->fmt)) return FP8_ERR_UNSUPPORTED;
+  const bool tensor = o->scaling == FP8_SCALE_TENSOR, mx = o->scaling == FP8_SCALE_MX_1x32;
+  if (checkpoint ? o->scaling != FP8_SCALE_BLOCK_1x128
+                 : !tensor && !mx && o->scaling != FP8_SCALE_BLOCK_1x128)
+    return FP8_ERR_UNSUPPORTED;
+  if (tensor && o->amax && !amax_ok) return FP8_ERR_UNSUPPORTED;
+  if (!have(o->data, n) || !have(tensor ? (const void*)o->scale : o->scale_inv, n))
+    return FP8_ERR_NULL;
+  if (!aligned(o->data, 16) || (tensor && (!aligned(o->scale, 4) || !aligned(o->amax, 4))) ||
+      (!tensor && !mx && !aligned(o->scale_inv, 4)))
+    return FP8_ERR_ALIGN;
+  return FP8_OK;
+}
+CastOut cast_out(const fp8_cast_out_t* o) {
+  CastOut c;
+  if (!o) return c;
+  c.q = o->data;
+  c.scale_inv = o->scale_inv;
+  c.scale = o->scale;
+  c.fmt = o->fmt;
+  c.scaling = o->scaling;
+  return c;
+}
+static_assert(fp8sg::kCastTensor == FP8_SCALE_TENSOR && fp8sg::kCastBlock == FP8_SCALE_BLOCK_1x128 &&
+                  fp8sg::kCastMX == FP8_SCALE_MX_1x32, "scalings");
+static_assert(fp8sg::kActGelu == FP8_ACT_GELU && fp8sg::kActGeluTanh == FP8_ACT_GELU_TANH &&
+                  fp8sg::kActSilu == FP8_ACT_SILU, "activations");
+// The amax that a tensor-scaled output asks for, or NULL.
+float* amax_of(const fp8_cast_out_t* o) {
+  return o && o->scaling == FP8_SCALE_TENSOR ? o->amax : nullptr;
+}
+// A checkpoint that is read: 1x128 tiles.
+fp8_status_t held_ok(const fp8_operand_t* o, int64_t n) {
+  if (!fmt_ok(o->fmt) || o->scaling != FP8_SCALE_BLOCK_1x128) return FP8_ERR_UNSUPPORTED;
+  if (!have(o->data, n) || !have(o->scale_inv, n)) return FP8_ERR_NULL;
+  if (!aligned(o->data, 16) || !aligned(o->scale_inv, 4)) return FP8_ERR_ALIGN;
+  return FP8_OK;
+}
+bool type_ok(int32_t t) { return t == FP8_TYPE_BF16 || t == FP8_TYPE_F32; }
+bool act_ok(int32_t act, int32_t gated) {
+  return act >= FP8_ACT_GELU && act <= FP8_ACT_SILU && (gated == 0 || gated == 1);
+}
+bool norm_dims_ok(int64_t rows, int64_t cols) {
+  return dims_ok(rows, cols) && cols >= 1 && cols <= fp8sg::kMaxNormCols;
+}
+bool moe_sizes_ok(int64_t n, int32_t experts, int32_t pad) {
+  return n >= 0 && n < kMaxDim && experts >= 1 && experts <= fp8sg::kMaxExperts && pad >= 1;
+}
+int64_t moe_rows(int64_t n, int32_t experts, int32_t pad) {
+  return (n + (n < experts ? n : experts) * ((int64_t)pad - 1)) / pad * pad;
+}
+// rows is below 2^31 because a row's number is an int32
+bool moe_dims_ok(int64_t tokens, int32_t k, int64_t cols, int64_t rows) {
+  return dims_ok(tokens, cols) && k >= 1 && tokens * (int64_t)k < kMaxDim && rows >= 0 &&
+         rows < kMaxDim;
+}
+
 }  // namespace
 
 extern "C" {
@@ -368,6 +430,250 @@ fp8_status_t fp8_convert_f32(const float* x, int64_t n, int32_t fmt, uint8_t* q,
   if (!have(x, n) || !have(q, n)) return FP8_ERR_NULL;
   if (!aligned(x, 16) || !aligned(q, 16)) return FP8_ERR_ALIGN;
   return hip(fp8sg::launch_convert(x, n, fmt, q, st(stream)));
+}
+
+fp8_status_t fp8_layernorm_fwd(const void* x, int32_t x_type, const void* gamma, const void* beta,
+                               int32_t w_type, int64_t rows, int64_t cols, float eps,
+                               void* y_bf16, float* mean, float* rstd, const fp8_cast_out_t* yq,
+                               const fp8_cast_out_t* xhat, void* workspace, void* stream) {
+  if (!gamma || !beta) return FP8_ERR_NULL;
+  if (!type_ok(x_type) || !type_ok(w_type)) return FP8_ERR_UNSUPPORTED;
+  if (!norm_dims_ok(rows, cols) || !(eps >= 0.0f && eps <= 3.402823466e+38f)) return FP8_ERR_SHAPE;
+  const int64_t n = rows * cols;
+  if (!have(x, n) || !have(mean, n) || !have(rstd, n) || (!y_bf16 && !yq && !xhat && n > 0))
+    return FP8_ERR_NULL;
+  fp8_status_t e = cast_out_ok(yq, false, true, n);
+  if (e == FP8_OK) e = cast_out_ok(xhat, true, false, n);
+  if (e != FP8_OK) return e;
+  float* amax = amax_of(yq);
+  if (amax && !workspace) return FP8_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(gamma, 16) || !aligned(beta, 16) || !aligned(y_bf16, 16) ||
+      !aligned(mean, 4) || !aligned(rstd, 4) || (amax && !aligned(workspace, 256)))
+    return FP8_ERR_ALIGN;
+  fp8sg::NormFwd p;
+  p.x = x;
+  p.gamma = gamma;
+  p.beta = beta;
+  p.x_type = x_type;
+  p.w_type = w_type;
+  p.rows = rows;
+  p.cols = (int)cols;
+  p.eps = eps;
+  p.y = static_cast<uint16_t*>(y_bf16);
+  p.mean = mean;
+  p.rstd = rstd;
+  p.yq = cast_out(yq);
+  p.xhat = cast_out(xhat);
+  p.amax = amax;
+  p.part = amax ? wsp(workspace) : nullptr;
+  return hip(fp8sg::launch_layernorm_fwd(p, st(stream)));
+}
+
+int64_t fp8_layernorm_workspace_bytes(int64_t rows, int64_t cols) {
+  if (!norm_dims_ok(rows, cols)) return 0;
+  return (int64_t)fp8sg::layernorm_bwd_partials(rows, cols) * 2 * cols * 4;
+}
+
+fp8_status_t fp8_layernorm_bwd(const void* dy_bf16, const void* x, int32_t x_type,
+                               const float* mean, const float* rstd, const fp8_operand_t* xhat,
+                               const void* gamma, int32_t w_type, int64_t rows, int64_t cols,
+                               void* dx, float* dgamma, float* dbeta, void* workspace,
+                               void* stream) {
+  if (!gamma || !dgamma || !dbeta) return FP8_ERR_NULL;
+  if (!type_ok(x_type) || !type_ok(w_type)) return FP8_ERR_UNSUPPORTED;
+  if (!norm_dims_ok(rows, cols)) return FP8_ERR_SHAPE;
+  const int64_t n = rows * cols;
+  if (!have(dy_bf16, n) || !have(dx, n) || !have(rstd, n) || !have(workspace, n))
+    return FP8_ERR_NULL;
+  if (xhat ? x != nullptr || mean != nullptr : !have(x, n) || !have(mean, n)) return FP8_ERR_NULL;
+  if (xhat) {
+    const fp8_status_t e = held_ok(xhat, n);
+    if (e != FP8_OK) return e;
+  }
+  if (!aligned(dy_bf16, 16) || !aligned(x, 16) || !aligned(mean, 4) || !aligned(rstd, 4) ||
+      !aligned(gamma, 16) || !aligned(dx, 16) || !aligned(dgamma, 4) || !aligned(dbeta, 4) ||
+      !aligned(workspace, 256))
+    return FP8_ERR_ALIGN;
+  fp8sg::NormBwd p;
+  p.dy = static_cast<const uint16_t*>(dy_bf16);
+  p.x = x;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.xhat = xhat ? xhat->data : nullptr;
+  p.xhat_scale = xhat ? static_cast<const float*>(xhat->scale_inv) : nullptr;
+  p.xhat_fmt = xhat ? xhat->fmt : 0;
+  p.gamma = gamma;
+  p.x_type = x_type;
+  p.w_type = w_type;
+  p.rows = rows;
+  p.cols = (int)cols;
+  p.dx = dx;
+  p.dgamma = dgamma;
+  p.dbeta = dbeta;
+  p.part = static_cast<float*>(workspace);
+  return hip(fp8sg::launch_layernorm_bwd(p, st(stream)));
+}
+
+fp8_status_t fp8_act_fwd(const void* h_bf16, int32_t act, int32_t gated, int64_t rows,
+                         int64_t cols, void* y_bf16, const fp8_cast_out_t* yq,
+                         const fp8_cast_out_t* ckpt, void* workspace, void* stream) {
+  if (!act_ok(act, gated)) return FP8_ERR_UNSUPPORTED;
+  if (!dims_ok(rows, cols)) return FP8_ERR_SHAPE;
+  const int64_t n = rows * cols;
+  if (!have(h_bf16, n) || (!y_bf16 && !yq && !ckpt && n > 0)) return FP8_ERR_NULL;
+  fp8_status_t e = cast_out_ok(yq, false, true, n);
+  if (e == FP8_OK) e = cast_out_ok(ckpt, true, false, n);
+  if (e != FP8_OK) return e;
+  float* amax = amax_of(yq);
+  if (amax && !workspace) return FP8_ERR_NULL;
+  if (!aligned(h_bf16, 16) || !aligned(y_bf16, 16) || (amax && !aligned(workspace, 256)))
+    return FP8_ERR_ALIGN;
+  fp8sg::ActFwd p;
+  p.h = static_cast<const uint16_t*>(h_bf16);
+  p.act = act;
+  p.gated = gated != 0;
+  p.rows = rows;
+  p.cols = cols;
+  p.y = static_cast<uint16_t*>(y_bf16);
+  p.yq = cast_out(yq);
+  p.ckpt = cast_out(ckpt);
+  p.amax = amax;
+  p.part = amax ? wsp(workspace) : nullptr;
+  return hip(fp8sg::launch_act_fwd(p, st(stream)));
+}
+
+fp8_status_t fp8_act_bwd(const void* dy_bf16, const void* h_bf16, const fp8_operand_t* ckpt,
+                         int32_t act, int32_t gated, int64_t rows, int64_t cols, void* dh_bf16,
+                         void* y_bf16, void* stream) {
+  if (!act_ok(act, gated)) return FP8_ERR_UNSUPPORTED;
+  if (!dims_ok(rows, cols)) return FP8_ERR_SHAPE;
+  const int64_t n = rows * cols;
+  if (!have(dy_bf16, n) || !have(dh_bf16, n)) return FP8_ERR_NULL;
+  if (ckpt ? h_bf16 != nullptr : !have(h_bf16, n)) return FP8_ERR_NULL;
+  if (ckpt) {
+    const fp8_status_t e = held_ok(ckpt, n);
+    if (e != FP8_OK) return e;
+  }
+  if (!aligned(dy_bf16, 16) || !aligned(h_bf16, 16) || !aligned(dh_bf16, 16) ||
+      !aligned(y_bf16, 16))
+    return FP8_ERR_ALIGN;
+  fp8sg::ActBwd p;
+  p.dy = static_cast<const uint16_t*>(dy_bf16);
+  p.h = static_cast<const uint16_t*>(h_bf16);
+  p.ckpt = ckpt ? ckpt->data : nullptr;
+  p.ckpt_scale = ckpt ? static_cast<const float*>(ckpt->scale_inv) : nullptr;
+  p.ckpt_fmt = ckpt ? ckpt->fmt : 0;
+  p.act = act;
+  p.gated = gated != 0;
+  p.rows = rows;
+  p.cols = cols;
+  p.dh = static_cast<uint16_t*>(dh_bf16);
+  p.y = static_cast<uint16_t*>(y_bf16);
+  return hip(fp8sg::launch_act_bwd(p, st(stream)));
+}
+
+fp8_status_t fp8_checkpoint_save(const void* x_bf16, int64_t rows, int64_t cols,
+                                 const fp8_cast_out_t* ckpt, void* stream) {
+  if (!ckpt) return FP8_ERR_NULL;
+  if (!dims_ok(rows, cols)) return FP8_ERR_SHAPE;
+  if (!have(x_bf16, rows * cols)) return FP8_ERR_NULL;
+  const fp8_status_t e = cast_out_ok(ckpt, true, false, rows * cols);
+  if (e != FP8_OK) return e;
+  if (!aligned(x_bf16, 16)) return FP8_ERR_ALIGN;
+  return hip(fp8sg::launch_checkpoint_save(static_cast<const uint16_t*>(x_bf16), rows, cols,
+                                           cast_out(ckpt), st(stream)));
+}
+
+fp8_status_t fp8_checkpoint_load(const fp8_operand_t* ckpt, int64_t rows, int64_t cols,
+                                 void* y_bf16, void* stream) {
+  if (!ckpt) return FP8_ERR_NULL;
+  if (!dims_ok(rows, cols)) return FP8_ERR_SHAPE;
+  const fp8_status_t e = held_ok(ckpt, rows * cols);
+  if (e != FP8_OK) return e;
+  if (!have(y_bf16, rows * cols)) return FP8_ERR_NULL;
+  if (!aligned(y_bf16, 16)) return FP8_ERR_ALIGN;
+  return hip(fp8sg::launch_checkpoint_load(ckpt->data, static_cast<const float*>(ckpt->scale_inv),
+                                           ckpt->fmt, rows, cols, static_cast<uint16_t*>(y_bf16),
+                                           st(stream)));
+}
+
+int64_t fp8_moe_rows(int64_t n, int32_t experts, int32_t pad) {
+  return moe_sizes_ok(n, experts, pad) ? moe_rows(n, experts, pad) : 0;
+}
+
+int64_t fp8_moe_workspace_bytes(int64_t n, int32_t experts) {
+  return moe_sizes_ok(n, experts, 1) ? fp8sg::moe_workspace_words(n, experts) * 4 : 0;
+}
+
+fp8_status_t fp8_moe_sort(const int32_t* expert, int64_t tokens, int32_t k, int32_t experts,
+                          int32_t pad, int64_t rows, int32_t* offsets, int32_t* counts,
+                          int32_t* pos, int32_t* src, void* workspace, void* stream) {
+  if (!offsets || !counts || !workspace) return FP8_ERR_NULL;
+  if (!moe_dims_ok(tokens, k, 0, rows)) return FP8_ERR_SHAPE;
+  const int64_t n = tokens * k;
+  if (!moe_sizes_ok(n, experts, pad) || moe_rows(n, experts, pad) > rows) return FP8_ERR_SHAPE;
+  if (!have(expert, n) || !have(pos, n) || !have(src, rows)) return FP8_ERR_NULL;
+  if (!aligned(expert, 4) || !aligned(offsets, 4) || !aligned(counts, 4) || !aligned(pos, 4) ||
+      !aligned(src, 4) || !aligned(workspace, 4))
+    return FP8_ERR_ALIGN;
+  return hip(fp8sg::launch_moe_sort(expert, n, experts, pad, rows, offsets, counts, pos, src,
+                                    wsp(workspace), st(stream)));
+}
+
+fp8_status_t fp8_moe_dispatch(const void* x_bf16, int64_t tokens, int32_t k, int64_t cols,
+                              const int32_t* pos, const int32_t* src, const int32_t* offsets,
+                              int32_t experts, int64_t rows, void* xs_bf16,
+                              const fp8_cast_out_t* xq, void* stream) {
+  if (!offsets) return FP8_ERR_NULL;
+  if (!moe_dims_ok(tokens, k, cols, rows) || experts < 1 || experts > fp8sg::kMaxExperts)
+    return FP8_ERR_SHAPE;
+  if (!have(x_bf16, tokens * cols) || !have(pos, tokens) || !have(src, rows) ||
+      (!xs_bf16 && !xq && rows * cols > 0))
+    return FP8_ERR_NULL;
+  const fp8_status_t e = cast_out_ok(xq, false, false, rows * cols);
+  if (e != FP8_OK) return e;
+  if (!aligned(x_bf16, 16) || !aligned(xs_bf16, 16) || !aligned(pos, 4) || !aligned(src, 4) ||
+      !aligned(offsets, 4))
+    return FP8_ERR_ALIGN;
+  const fp8sg::MoeRows p{pos, src, offsets + experts, tokens, rows, k, cols};
+  return hip(fp8sg::launch_moe_dispatch(p, static_cast<const uint16_t*>(x_bf16),
+                                        static_cast<uint16_t*>(xs_bf16), cast_out(xq),
+                                        st(stream)));
+}
+
+fp8_status_t fp8_moe_combine(const void* ys_bf16, const int32_t* pos, const float* weight,
+                             int64_t tokens, int32_t k, int64_t cols, int64_t rows, void* y_bf16,
+                             void* stream) {
+  if (!moe_dims_ok(tokens, k, cols, rows)) return FP8_ERR_SHAPE;
+  if (!have(ys_bf16, rows * cols) || !have(pos, tokens) || !have(y_bf16, tokens * cols))
+    return FP8_ERR_NULL;
+  if (!aligned(ys_bf16, 16) || !aligned(y_bf16, 16) || !aligned(pos, 4) || !aligned(weight, 4))
+    return FP8_ERR_ALIGN;
+  const fp8sg::MoeRows p{pos, nullptr, nullptr, tokens, rows, k, cols};
+  return hip(fp8sg::launch_moe_combine(p, static_cast<const uint16_t*>(ys_bf16), weight,
+                                       static_cast<uint16_t*>(y_bf16), st(stream)));
+}
+
+fp8_status_t fp8_moe_combine_bwd(const void* dy_bf16, const void* ys_bf16, const float* weight,
+                                 const int32_t* pos, const int32_t* src, const int32_t* offsets,
+                                 int64_t tokens, int32_t k, int64_t cols, int32_t experts,
+                                 int64_t rows, void* dys_bf16, float* dweight, void* stream) {
+  if (!offsets) return FP8_ERR_NULL;
+  if (!moe_dims_ok(tokens, k, cols, rows) || experts < 1 || experts > fp8sg::kMaxExperts)
+    return FP8_ERR_SHAPE;
+  if (!have(dy_bf16, tokens * cols) || !have(ys_bf16, rows * cols) || !have(weight, tokens) ||
+      !have(pos, tokens) || !have(src, rows) || !have(dys_bf16, rows * cols) ||
+      !have(dweight, tokens))
+    return FP8_ERR_NULL;
+  if (!aligned(dy_bf16, 16) || !aligned(ys_bf16, 16) || !aligned(dys_bf16, 16) ||
+      !aligned(weight, 4) || !aligned(pos, 4) || !aligned(src, 4) || !aligned(offsets, 4) ||
+      !aligned(dweight, 4))
+    return FP8_ERR_ALIGN;
+  const fp8sg::MoeRows p{pos, src, offsets + experts, tokens, rows, k, cols};
+  return hip(fp8sg::launch_moe_combine_bwd(p, static_cast<const uint16_t*>(dy_bf16),
+                                           static_cast<const uint16_t*>(ys_bf16), weight,
+                                           static_cast<uint16_t*>(dys_bf16), dweight,
+                                           st(stream)));
 }
 
 const char* fp8_status_string(fp8_status_t status) {

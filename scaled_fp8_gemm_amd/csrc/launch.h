@@ -94,6 +94,111 @@ hipError_t launch_quantize_t(const void* x, int64_t rows, int64_t cols, int fmt,
                              uint8_t* q, void* sq, uint8_t* qT, void* sqT, hipStream_t s);
 hipError_t launch_convert(const float* x, int64_t n, int fmt, uint8_t* q, hipStream_t s);
 
+// A cast of 32-bit results to FP8 as an output of a row operator.  scaling:
+// absent, one scale for the tensor (scale, given), one per row and 128
+// columns (float, written), or one per row and 32 columns (E8M0, written);
+// the last tile of a row may be short.
+enum : int { kCastNone = -1, kCastTensor = 0, kCastBlock = 1, kCastMX = 3 };
+struct CastOut {
+  uint8_t* q = nullptr;
+  void* scale_inv = nullptr;
+  const float* scale = nullptr;
+  int fmt = 0;
+  int scaling = kCastNone;
+};
+
+// Layer norm over rows of cols (1 .. kMaxNormCols) elements.  Types: 0 BF16, 1 FP32.
+constexpr int64_t kMaxNormCols = 32768;
+struct NormFwd {
+  const void* x;
+  const void* gamma;
+  const void* beta;
+  int x_type, w_type;
+  int64_t rows;
+  int cols;
+  float eps;
+  uint16_t* y;            // BF16, or NULL
+  float* mean;
+  float* rstd;
+  CastOut yq, xhat;       // xhat: kCastBlock or absent
+  float* amax;            // amax of y (with yq per tensor), or NULL
+  uint32_t* part;         // its partial maxima (the caller's workspace)
+};
+hipError_t launch_layernorm_fwd(const NormFwd& p, hipStream_t s);
+struct NormBwd {
+  const uint16_t* dy;
+  const void* x;          // NULL: the normalised rows come from xhat
+  const float* mean;      // with x
+  const float* rstd;
+  const uint8_t* xhat;
+  const float* xhat_scale;
+  int xhat_fmt;
+  const void* gamma;
+  int x_type, w_type;     // x_type: of x and dx
+  int64_t rows;
+  int cols;
+  void* dx;
+  float* dgamma;
+  float* dbeta;
+  float* part;            // layernorm_bwd_partials() rows of 2 * cols floats
+};
+// Workgroups of the backward pass, each with one row of partial sums.
+int layernorm_bwd_partials(int64_t rows, int64_t cols);
+hipError_t launch_layernorm_bwd(const NormBwd& p, hipStream_t s);
+
+// Activations between two GEMMs, and their 8-bit checkpoints.
+enum : int { kActGelu = 0, kActGeluTanh = 1, kActSilu = 2 };
+struct ActFwd {
+  const uint16_t* h;      // [rows][cols], gated: [rows][2 * cols] = [a | u]
+  int act;
+  bool gated;
+  int64_t rows, cols;
+  uint16_t* y;            // [rows][cols] BF16, or NULL
+  CastOut yq;             // of y, or absent
+  CastOut ckpt;           // of h as [rows * (1 + gated)][cols], kCastBlock or absent
+  float* amax;            // amax of y (with yq per tensor), or NULL
+  uint32_t* part;         // its partial maxima (the caller's workspace)
+};
+hipError_t launch_act_fwd(const ActFwd& p, hipStream_t s);
+struct ActBwd {
+  const uint16_t* dy;
+  const uint16_t* h;      // NULL: from the checkpoint
+  const uint8_t* ckpt;
+  const float* ckpt_scale;
+  int ckpt_fmt;
+  int act;
+  bool gated;
+  int64_t rows, cols;
+  uint16_t* dh;
+  uint16_t* y;            // the forward pass's output again, or NULL
+};
+hipError_t launch_act_bwd(const ActBwd& p, hipStream_t s);
+hipError_t launch_checkpoint_save(const uint16_t* x, int64_t rows, int64_t cols, const CastOut& o,
+                                  hipStream_t s);
+hipError_t launch_checkpoint_load(const uint8_t* q, const float* scale_inv, int fmt, int64_t rows,
+                                  int64_t cols, uint16_t* y, hipStream_t s);
+
+// Tokens sorted by expert.  n = tokens * k choices.
+constexpr int kMaxExperts = 1024;
+int64_t moe_workspace_words(int64_t n, int experts);
+hipError_t launch_moe_sort(const int32_t* expert, int64_t n, int experts, int pad, int64_t rows,
+                           int32_t* offsets, int32_t* counts, int32_t* pos, int32_t* src,
+                           uint32_t* ws, hipStream_t s);
+struct MoeRows {
+  const int32_t* pos;     // [tokens][k]: row of the sorted rows, or dropped (outside [0, rows))
+  const int32_t* src;     // [rows]: choice t * k + j, or none (negative)
+  const int32_t* end;     // offsets[experts]: rows in use
+  int64_t tokens, rows;
+  int k;
+  int64_t cols;
+};
+hipError_t launch_moe_dispatch(const MoeRows& p, const uint16_t* x, uint16_t* xs,
+                               const CastOut& xq, hipStream_t s);
+hipError_t launch_moe_combine(const MoeRows& p, const uint16_t* ys, const float* weight,
+                              uint16_t* y, hipStream_t s);
+hipError_t launch_moe_combine_bwd(const MoeRows& p, const uint16_t* dy, const uint16_t* ys,
+                                  const float* weight, uint16_t* dys, float* dw, hipStream_t s);
+
 // C[M][N] (BF16) = A[M][K] . B[N][K]^T with the operands' scales.
 // mode: 0 tensor, 1 block (bra/brb = 1 or 128 rows per scale), 2 MX.
 struct GemmProblem {

@@ -31,12 +31,6 @@ constexpr int kThreads = 256;
 // workgroup c mod gridDim.x; the last chunk is predicated.
 constexpr int kChunkLoads = 4;
 
-// Input element types: BF16 (the activations, gradients and BF16 master
-// weights) or FP32 (an FP32 master weight).  Maxima are kept as FP32
-// magnitude bits (a BF16 magnitude shifted left by 16), which order like the
-// values: NaN > inf > finite.
-enum : int { kInBF16 = 0, kInF32 = 1 };
-
 // Largest magnitude (FP32 bits) in one 16-byte vector of either type.
 template <int IN>
 __device__ __forceinline__ uint32_t vec_absmax(uint4 v) {
@@ -783,21 +777,7 @@ __global__ __launch_bounds__(kThreads) void k_block_128(const uint16_t* __restri
 }
 
 // MX 1x32: block b covers elements [32b, 32b+32) (cols % 32 == 0), handled by
-// 4 lanes with one 16-byte load each.  The shared exponent is computed with
-// integer operations on the FP32 bits of the block's BF16 amax a:
-//   a = (1 + f) * 2^(E-127) with biased exponent E and fraction f; writing
-//   fmax = 1.75 * 2^P (P = 8 for E4M3, 15 for E5M2), the smallest integer e
-//   with a <= fmax * 2^e is (E - 127) - P when 1 + f <= 1.75 (fraction field
-//   <= 0x600000), else one more; clamped to [-127, 127].  Subnormal amax
-//   (E = 0) is far below fmax * 2^-127 and gets -127.
-template <int FMT>
-__device__ __forceinline__ int mx_exponent_bits(uint32_t abits) {
-  const int E = (int)(abits >> 23);
-  const uint32_t frac = abits & 0x7fffffu;
-  int e = (E - 127) - FmtTraits<FMT>::max_exp + (frac > 0x600000u ? 1 : 0);
-  if (E == 0) e = -127;
-  return min(127, max(-127, e));
-}
+// 4 lanes with one 16-byte load each.
 
 // Scale 2^-e of an MX block from its BF16 magnitude bits m, and the E8M0
 // byte: inf/NaN in the block -> 0xFF (elements cast unscaled), all-zero ->
@@ -888,12 +868,6 @@ __device__ __forceinline__ uint32_t pmax16(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a),
                                                                 __builtin_bit_cast(u16x2_t, b)));
 }
-// DPP lane move inside rows of 16 lanes (quad_perm / row_ror controls).
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
-}
-constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppRor4 = 0x124, kDppRor8 = 0x128;
 // Maximum over the lanes l, l ^ 16, l ^ 32, l ^ 48 (one column block of a wave).
 __device__ __forceinline__ uint32_t rows_max(uint32_t v) {
   auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);

@@ -26,6 +26,11 @@ SCALE_TENSOR = 0
 SCALE_BLOCK_1x128 = 1
 SCALE_BLOCK_128x128 = 2
 SCALE_MX_1x32 = 3
+TYPE_BF16 = 0
+TYPE_F32 = 1
+ACT_GELU = 0
+ACT_GELU_TANH = 1
+ACT_SILU = 2
 
 # FP8_WORKSPACE_BYTES of include/fp8sg.h
 WORKSPACE_BYTES = 295552
@@ -46,6 +51,13 @@ class Operand(ctypes.Structure):
     """fp8_operand_t: FP8 data [rows][K], format, scaling and scale_inv."""
     _fields_ = [("data", ctypes.c_void_p), ("fmt", ctypes.c_int32),
                 ("scaling", ctypes.c_int32), ("scale_inv", ctypes.c_void_p)]
+
+
+class CastOut(ctypes.Structure):
+    """fp8_cast_out_t: an FP8 output of a row operator."""
+    _fields_ = [("data", ctypes.c_void_p), ("fmt", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("scale_inv", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("amax", ctypes.c_void_p)]
 
 
 _lib = None
@@ -81,11 +93,28 @@ def lib():
             "fp8_gemm_wgrad_f32": [vp, vp, i64, i64, i64, vp, i32, vp],
             "fp8_gemm_fprop_fused": [vp, vp, i64, i64, i64, vp, i32, vp, vp, vp, vp, vp],
             "fp8_convert_f32": [vp, i64, i32, vp, vp],
+            "fp8_layernorm_fwd": [vp, i32, vp, vp, i32, i64, i64, ctypes.c_float, vp, vp, vp, vp,
+                                  vp, vp, vp],
+            "fp8_layernorm_bwd": [vp, vp, i32, vp, vp, vp, vp, i32, i64, i64, vp, vp, vp, vp, vp],
+            "fp8_act_fwd": [vp, i32, i32, i64, i64, vp, vp, vp, vp, vp],
+            "fp8_act_bwd": [vp, vp, vp, i32, i32, i64, i64, vp, vp, vp],
+            "fp8_checkpoint_save": [vp, i64, i64, vp, vp],
+            "fp8_checkpoint_load": [vp, i64, i64, vp, vp],
+            "fp8_moe_sort": [vp, i64, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp],
+            "fp8_moe_dispatch": [vp, i64, i32, i64, vp, vp, vp, i32, i64, vp, vp, vp],
+            "fp8_moe_combine": [vp, vp, vp, i64, i32, i64, i64, vp, vp],
+            "fp8_moe_combine_bwd": [vp, vp, vp, vp, vp, vp, i64, i32, i64, i32, i64, vp, vp, vp],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
             fn.argtypes = args
             fn.restype = ctypes.c_int
+        for name, args in {"fp8_layernorm_workspace_bytes": [i64, i64],
+                           "fp8_moe_rows": [i64, i32, i32],
+                           "fp8_moe_workspace_bytes": [i64, i32]}.items():
+            fn = getattr(L, name)
+            fn.argtypes = args
+            fn.restype = ctypes.c_int64
         L.fp8_status_string.argtypes = [ctypes.c_int]
         L.fp8_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -96,6 +125,8 @@ def lib():
 _BF16 = (torch.bfloat16, torch.int16)
 _F32 = (torch.float32,)
 _U8 = (torch.uint8,)
+_I32 = (torch.int32,)
+_BF16_F32 = _BF16 + _F32
 
 
 def _t(x, name, dtypes, numel, optional=False):
@@ -383,6 +414,233 @@ def fp8_gemm_wgrad_f32(dyT: Operand, xT: Operand, M, N, K, dw, accumulate=False,
     _check("fp8_gemm_wgrad_f32",
            lib().fp8_gemm_wgrad_f32(ctypes.byref(dyT), ctypes.byref(xT), M, N, K, dwp,
                                     1 if accumulate else 0, _stream(stream)))
+
+
+# ------------------------------------------------------------ row operators
+def cast_out(data, fmt, scaling, scale_inv=None, scale=None, amax=None) -> CastOut:
+    """An FP8 output of a row operator: `scale_inv` receives the scales of
+    1x128 tiles (FP32) or 1x32 MX blocks (E8M0 bytes); per-tensor scaling
+    takes `scale` and may ask for `amax`.  Holds its tensors, as operand()
+    does; sizes are checked by the call that knows the rows and columns."""
+    o = CastOut(data.data_ptr(), fmt, scaling, None if scale_inv is None else scale_inv.data_ptr(),
+                None if scale is None else scale.data_ptr(),
+                None if amax is None else amax.data_ptr())
+    o._tensors = (data, scale_inv, scale, amax)
+    return o
+
+
+def _check_cast_out(o, name, rows, cols, halves=1):
+    """Checks an FP8 output of [rows][halves * cols] (tiles of each half of
+    their own); returns the reference the C call takes."""
+    if o is None:
+        return None
+    data, sc, scale, amax = o._tensors
+    _t(data, f"{name}.data", _U8, rows * cols * halves)
+    if o.scaling == SCALE_TENSOR:
+        _t(scale, f"{name}.scale", _F32, 1)
+        _t(amax, f"{name}.amax", _F32, 1, True)
+    elif o.scaling == SCALE_BLOCK_1x128:
+        _t(sc, f"{name}.scale_inv", _F32, rows * halves * _blocks(cols, 128))
+    elif o.scaling == SCALE_MX_1x32:
+        _t(sc, f"{name}.scale_inv", _U8, rows * halves * _blocks(cols, 32))
+    return ctypes.byref(o)
+
+
+def _wants_amax(o):
+    return o is not None and o.scaling == SCALE_TENSOR and o.amax is not None
+
+
+def _held(o: Operand, name, rows, cols):
+    """Checks a checkpoint of [rows][cols] that a call reads."""
+    _check_operand(o, name, rows, cols)
+    return ctypes.byref(o)
+
+
+def _float_type(x):
+    return TYPE_F32 if x.dtype == torch.float32 else TYPE_BF16
+
+
+def fp8_layernorm_fwd(x, gamma, beta, eps, y, mean, rstd, yq=None, xhat=None, stream=None,
+                      workspace=None):
+    """Layer norm over the rows of x (BF16 or FP32) with gamma and beta (both
+    BF16 or both FP32): y (BF16, or None), the rows' mean and rstd, y cast to
+    FP8 (`yq`) and the normalised rows in 8 bits for the backward pass
+    (`xhat`), both from cast_out()."""
+    rows, cols = _rc(x)
+    n = rows * cols
+    ws = _Ws(workspace, stream) if _wants_amax(yq) else None
+    if isinstance(beta, torch.Tensor) and beta.dtype != gamma.dtype:
+        raise ValueError(f"beta has dtype {beta.dtype}, gamma {gamma.dtype}")
+    _check("fp8_layernorm_fwd",
+           lib().fp8_layernorm_fwd(_t(x, "x", _BF16_F32, n), _float_type(x),
+                                   _t(gamma, "gamma", _BF16_F32, cols),
+                                   _t(beta, "beta", _BF16_F32, cols), _float_type(gamma), rows,
+                                   cols, eps, _t(y, "y", _BF16, n, True),
+                                   _t(mean, "mean", _F32, rows), _t(rstd, "rstd", _F32, rows),
+                                   _check_cast_out(yq, "yq", rows, cols),
+                                   _check_cast_out(xhat, "xhat", rows, cols),
+                                   ws.ptr if ws else None, _stream(stream)))
+
+
+def layernorm_workspace(rows, cols, device=None) -> torch.Tensor:
+    """fp8_layernorm_bwd's workspace for these sizes (any contents)."""
+    dev = torch.device("cuda") if device is None else torch.device(device)
+    return torch.empty(max(4, lib().fp8_layernorm_workspace_bytes(rows, cols)),
+                       dtype=torch.uint8, device=dev)
+
+
+def fp8_layernorm_bwd(dy, x, mean, rstd, gamma, dx, dgamma, dbeta, xhat=None, stream=None,
+                      workspace=None):
+    """Gradients of fp8_layernorm_fwd from x and mean, or from the checkpoint
+    `xhat` (an operand(); x and mean are then None).  `workspace`: from
+    layernorm_workspace(); None takes a fresh one for this call."""
+    rows, cols = _rc(dy, "dy")
+    n = rows * cols
+    if workspace is None:
+        workspace = layernorm_workspace(rows, cols, dy.device)
+        if isinstance(stream, torch.cuda.Stream):
+            workspace.record_stream(stream)
+        elif stream is not None:
+            raise ValueError("pass a workspace when the stream is a raw handle")
+    if isinstance(x, torch.Tensor) and x.dtype != dx.dtype:
+        raise ValueError(f"dx has dtype {dx.dtype}, x {x.dtype}")
+    held = None if xhat is None else _held(xhat, "xhat", rows, cols)
+    _check("fp8_layernorm_bwd",
+           lib().fp8_layernorm_bwd(
+               _t(dy, "dy", _BF16, n), _t(x, "x", _BF16_F32, n, held is not None),
+               _float_type(dx), _t(mean, "mean", _F32, rows, held is not None),
+               _t(rstd, "rstd", _F32, rows), held, _t(gamma, "gamma", _BF16_F32, cols),
+               _float_type(gamma), rows, cols, _t(dx, "dx", _BF16_F32, n),
+               _t(dgamma, "dgamma", _F32, cols), _t(dbeta, "dbeta", _F32, cols),
+               _t(workspace, "workspace", _U8, lib().fp8_layernorm_workspace_bytes(rows, cols)),
+               _stream(stream)))
+
+
+def _halves(wide, gated, name):
+    rows, width = _rc(wide, name)
+    if not gated:
+        return rows, width
+    if width % 2:
+        raise ValueError(f"{name} holds [a | u]: its width {width} must be even")
+    return rows, width // 2
+
+
+def fp8_act_fwd(h, act, gated, y, yq=None, ckpt=None, stream=None, workspace=None):
+    """y = act(h), or act(a) * u with h = [a | u] (`gated`): as BF16 (`y`, or
+    None), cast to FP8 (`yq`), and h in 8 bits for the backward pass (`ckpt`,
+    scales [rows * (1 + gated)][ceil(cols / 128)]), both from cast_out()."""
+    rows, cols = _halves(h, gated, "h")
+    ws = _Ws(workspace, stream) if _wants_amax(yq) else None
+    _check("fp8_act_fwd",
+           lib().fp8_act_fwd(_t(h, "h", _BF16, h.numel()), act, 1 if gated else 0, rows, cols,
+                             _t(y, "y", _BF16, rows * cols, True),
+                             _check_cast_out(yq, "yq", rows, cols),
+                             _check_cast_out(ckpt, "ckpt", rows, cols, 2 if gated else 1),
+                             ws.ptr if ws else None, _stream(stream)))
+
+
+def fp8_act_bwd(dy, h, act, gated, dh, y=None, stream=None):
+    """dh from dy and the forward pass's input h, a tensor or its checkpoint
+    (an operand()); `y`: the forward pass's output again."""
+    rows, cols = _rc(dy, "dy")
+    n, width = rows * cols, 2 if gated else 1
+    held = _held(h, "h", rows * width, cols) if isinstance(h, Operand) else None
+    _check("fp8_act_bwd",
+           lib().fp8_act_bwd(_t(dy, "dy", _BF16, n),
+                             None if held is not None else _t(h, "h", _BF16, n * width), held, act,
+                             1 if gated else 0, rows, cols, _t(dh, "dh", _BF16, n * width),
+                             _t(y, "y", _BF16, n, True), _stream(stream)))
+
+
+def fp8_checkpoint_save(x, ckpt: CastOut, stream=None):
+    rows, cols = _rc(x)
+    _check("fp8_checkpoint_save",
+           lib().fp8_checkpoint_save(_t(x, "x", _BF16, rows * cols), rows, cols,
+                                     _check_cast_out(ckpt, "ckpt", rows, cols), _stream(stream)))
+
+
+def fp8_checkpoint_load(ckpt: Operand, rows, cols, y, stream=None):
+    _check("fp8_checkpoint_load",
+           lib().fp8_checkpoint_load(_held(ckpt, "ckpt", rows, cols), rows, cols,
+                                     _t(y, "y", _BF16, rows * cols), _stream(stream)))
+
+
+def moe_rows(n, experts, pad) -> int:
+    """Rows that hold any sort of n choices (fp8_moe_rows)."""
+    return lib().fp8_moe_rows(n, experts, pad)
+
+
+def moe_workspace(n, experts, device=None) -> torch.Tensor:
+    """fp8_moe_sort's workspace for n = tokens * k choices (any contents)."""
+    dev = torch.device("cuda") if device is None else torch.device(device)
+    return torch.empty(max(4, lib().fp8_moe_workspace_bytes(n, experts)), dtype=torch.uint8,
+                       device=dev)
+
+
+def fp8_moe_sort(expert, experts, pad, offsets, counts, pos, src, stream=None, workspace=None):
+    """Sort the choices expert[tokens][k] (int32): see fp8_moe_sort in
+    include/fp8sg.h.  src holds moe_rows(tokens * k, experts, pad) rows or
+    more.  `workspace`: from moe_workspace(); None takes a fresh one."""
+    tokens, k = _rc(expert, "expert")
+    n = tokens * k
+    if workspace is None:
+        workspace = moe_workspace(n, experts, expert.device)
+        if isinstance(stream, torch.cuda.Stream):
+            workspace.record_stream(stream)
+        elif stream is not None:
+            raise ValueError("pass a workspace when the stream is a raw handle")
+    _check("fp8_moe_sort",
+           lib().fp8_moe_sort(_t(expert, "expert", _I32, n), tokens, k, experts, pad, src.numel(),
+                              _t(offsets, "offsets", _I32, experts + 1),
+                              _t(counts, "counts", _I32, experts), _t(pos, "pos", _I32, n),
+                              _t(src, "src", _I32, 0),
+                              _t(workspace, "workspace", _U8,
+                                 lib().fp8_moe_workspace_bytes(n, experts)), _stream(stream)))
+
+
+def _moe_rows_of(pos, src, offsets):
+    tokens, k = _rc(pos, "pos")
+    return (tokens, k, src.numel(), offsets.numel() - 1, _t(pos, "pos", _I32, tokens * k),
+            _t(src, "src", _I32, 0), _t(offsets, "offsets", _I32, 2))
+
+
+def fp8_moe_dispatch(x, pos, src, offsets, xs, xq=None, stream=None):
+    """Rows of x to their experts' segments: xs (BF16, or None) and / or cast
+    to FP8 (`xq`, from cast_out()), of src.numel() rows."""
+    rows_x, cols = _rc(x)
+    tokens, k, rows, experts, pp, sp, op = _moe_rows_of(pos, src, offsets)
+    if rows_x != tokens:
+        raise ValueError(f"x has {rows_x} rows, pos {tokens}")
+    _check("fp8_moe_dispatch",
+           lib().fp8_moe_dispatch(_t(x, "x", _BF16, tokens * cols), tokens, k, cols, pp, sp, op,
+                                  experts, rows, _t(xs, "xs", _BF16, rows * cols, True),
+                                  _check_cast_out(xq, "xq", rows, cols), _stream(stream)))
+
+
+def fp8_moe_combine(ys, pos, weight, y, stream=None):
+    """y[t] = sum_j weight[t][j] ys[pos[t][j]]; weight None: all 1 (the
+    gradient of fp8_moe_dispatch)."""
+    rows, cols = _rc(ys, "ys")
+    tokens, k = _rc(pos, "pos")
+    _check("fp8_moe_combine",
+           lib().fp8_moe_combine(_t(ys, "ys", _BF16, rows * cols),
+                                 _t(pos, "pos", _I32, tokens * k),
+                                 _t(weight, "weight", _F32, tokens * k, True), tokens, k, cols,
+                                 rows, _t(y, "y", _BF16, tokens * cols), _stream(stream)))
+
+
+def fp8_moe_combine_bwd(dy, ys, weight, pos, src, offsets, dys, dweight, stream=None):
+    """Gradients of fp8_moe_combine: dys (rows as ys) and dweight."""
+    rows_dy, cols = _rc(dy, "dy")
+    tokens, k, rows, experts, pp, sp, op = _moe_rows_of(pos, src, offsets)
+    if rows_dy != tokens:
+        raise ValueError(f"dy has {rows_dy} rows, pos {tokens}")
+    _check("fp8_moe_combine_bwd",
+           lib().fp8_moe_combine_bwd(_t(dy, "dy", _BF16, tokens * cols),
+                                     _t(ys, "ys", _BF16, rows * cols),
+                                     _t(weight, "weight", _F32, tokens * k), pp, sp, op, tokens,
+                                     k, cols, experts, rows, _t(dys, "dys", _BF16, rows * cols),
+                                     _t(dweight, "dweight", _F32, tokens * k), _stream(stream)))
 
 
 def fp8_convert_f32(x, fmt, q, stream=None):
