@@ -471,7 +471,7 @@ fp8_status_t fp8_layernorm_fwd(const void* x, int32_t x_type, const void* gamma,
 
 int64_t fp8_layernorm_workspace_bytes(int64_t rows, int64_t cols) {
   if (!norm_dims_ok(rows, cols)) return 0;
-  return (int64_t)fp8sg::layernorm_bwd_partials(rows, cols) * 2 * cols * 4;
+  return (int64_t)fp8sg::layernorm_bwd_partials(rows) * 2 * cols * 4;
 }
 
 fp8_status_t fp8_layernorm_bwd(const void* dy_bf16, const void* x, int32_t x_type,

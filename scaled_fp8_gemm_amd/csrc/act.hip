@@ -104,10 +104,10 @@ __global__ __launch_bounds__(kThreads) void k_act_fwd(const ActFwd p) {
     const int64_t left = p.cols - (int64_t)slot * 8;
     const int nv = left < 8 ? (int)left : 8;
     const int64_t col = (int64_t)slot * 8;
-    const uint16_t* hr = p.h + w.row * p.cols * (GATED ? 2 : 1) + col;
+    const uint16_t* hr = p.h + w.row * p.cols * (GATED ? 2 : 1);
     Slot<kInBF16> ha, hu;
-    ha.load(reinterpret_cast<const uint8_t*>(hr), nv);
-    if constexpr (GATED) hu.load(reinterpret_cast<const uint8_t*>(hr + p.cols), nv);
+    ha.load(hr, col, p.cols);
+    if constexpr (GATED) hu.load(hr + p.cols, col, p.cols);
     float a[8], u[8], y[8], q[8], d[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] = ha.get(i);
@@ -121,8 +121,8 @@ __global__ __launch_bounds__(kThreads) void k_act_fwd(const ActFwd p) {
       }
     }
     if (p.ckpt.q) {
-      cast_store(p.ckpt, a, w.row * (GATED ? 2 : 1), p.cols, slot, nv, 1.0f);
-      if constexpr (GATED) cast_store(p.ckpt, u, w.row * 2 + 1, p.cols, slot, nv, 1.0f);
+      cast_store_tile(p.ckpt, a, w.row * (GATED ? 2 : 1), p.cols, slot, nv);
+      if constexpr (GATED) cast_store_tile(p.ckpt, u, w.row * 2 + 1, p.cols, slot, nv);
     }
     if (p.y && nv > 0) store_bf16x8(p.y + w.row * p.cols + col, y, nv);
     if (p.yq.q) cast_store(p.yq, y, w.row, p.cols, slot, nv, ts);
@@ -147,21 +147,21 @@ __global__ __launch_bounds__(kThreads) void k_act_bwd(const ActBwd p) {
     if (nv <= 0) continue;
     const int64_t hrow = w.row * (GATED ? 2 : 1);
     Slot<kInBF16> g;
-    g.load(reinterpret_cast<const uint8_t*>(p.dy + w.row * p.cols + col), nv);
+    g.load(p.dy + w.row * p.cols, col, p.cols);
     float a[8], u[8], y[8], da[8], du[8], q[8], d[8];
     if constexpr (HELD) {
-      const uint8_t* held = p.ckpt + hrow * p.cols + col;
+      const uint8_t* held = p.ckpt + hrow * p.cols;
       const float* sc = p.ckpt_scale + hrow * tiles + w.tile;
-      const uint2 ba = load_u8x8(held, nv);
-      const uint2 bu = GATED ? load_u8x8(held + p.cols, nv) : make_uint2(0, 0);
+      const uint2 ba = load_u8x8(held, col, p.cols);
+      const uint2 bu = GATED ? load_u8x8(held + p.cols, col, p.cols) : make_uint2(0, 0);
       const float sa = sc[0], su = GATED ? sc[tiles] : 0.0f;
       decode8(p.ckpt_fmt, ba, sa, a);
       if constexpr (GATED) decode8(p.ckpt_fmt, bu, su, u);
     } else {
-      const uint16_t* hr = p.h + hrow * p.cols + col;
+      const uint16_t* hr = p.h + hrow * p.cols;
       Slot<kInBF16> ha, hu;
-      ha.load(reinterpret_cast<const uint8_t*>(hr), nv);
-      if constexpr (GATED) hu.load(reinterpret_cast<const uint8_t*>(hr + p.cols), nv);
+      ha.load(hr, col, p.cols);
+      if constexpr (GATED) hu.load(hr + p.cols, col, p.cols);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         a[i] = ha.get(i);
@@ -198,11 +198,11 @@ __global__ __launch_bounds__(kThreads) void k_ckpt_save(const uint16_t* __restri
     const int64_t left = cols - (int64_t)slot * 8;
     const int nv = left < 8 ? (int)left : 8;
     Slot<kInBF16> s;
-    s.load(reinterpret_cast<const uint8_t*>(x + w.row * cols + (int64_t)slot * 8), nv);
+    s.load(x + w.row * cols, (int64_t)slot * 8, cols);
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = s.get(i);
-    cast_store(o, v, w.row, cols, slot, nv, 1.0f);
+    cast_store_tile(o, v, w.row, cols, slot, nv);
   }
 }
 
@@ -221,7 +221,7 @@ __global__ __launch_bounds__(kThreads) void k_ckpt_load(const uint8_t* __restric
     if (nv <= 0) continue;
     const int64_t at = w.row * cols + col;
     float v[8];
-    decode8(fmt, load_u8x8(q + at, nv), scale_inv[w.row * tiles + w.tile], v);
+    decode8(fmt, load_u8x8(q + w.row * cols, col, cols), scale_inv[w.row * tiles + w.tile], v);
     store_bf16x8(y + at, v, nv);
   }
 }

@@ -142,8 +142,8 @@ struct NormBwd {
   float* dbeta;
   float* part;            // layernorm_bwd_partials() rows of 2 * cols floats
 };
-// Workgroups of the backward pass, each with one row of partial sums.
-int layernorm_bwd_partials(int64_t rows, int64_t cols);
+// The most workgroups of the backward pass, each with one row of partial sums.
+int layernorm_bwd_partials(int64_t rows);
 hipError_t launch_layernorm_bwd(const NormBwd& p, hipStream_t s);
 
 // Activations between two GEMMs, and their 8-bit checkpoints.

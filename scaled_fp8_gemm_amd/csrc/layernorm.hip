@@ -31,17 +31,26 @@ __device__ __forceinline__ float row_sum(float v, float* red, int nw) {
   return s;
 }
 
-// gamma / beta of a slot: BF16 or FP32, widened
-__device__ __forceinline__ void load_weight8(const void* w, int type, int col, int nv,
+// t, but not known to be the same in the next round of a loop: what a slot's
+// place in its row implies (offsets, masks) is worked out again for each row
+// rather than kept in registers, where it would push the row itself out.
+__device__ __forceinline__ int afresh(int t) {
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
+// gamma / beta of a slot: BF16 or FP32, widened.  Every row reads them
+// again, so they stay in the caches (no streaming loads).
+__device__ __forceinline__ void load_weight8(const void* w, int type, int col, int cols,
                                              float (&v)[8]) {
   if (type == kInBF16) {
     Slot<kInBF16> s;
-    s.load(static_cast<const uint8_t*>(w) + (int64_t)col * 2, nv);
+    s.load_cached(static_cast<const uint8_t*>(w), col, cols);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = s.get(i);
   } else {
     Slot<kInF32> s;
-    s.load(static_cast<const uint8_t*>(w) + (int64_t)col * 4, nv);
+    s.load_cached(static_cast<const uint8_t*>(w), col, cols);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = s.get(i);
   }
@@ -50,41 +59,52 @@ __device__ __forceinline__ void load_weight8(const void* w, int type, int col, i
 // Forward.  A row's threads (a wave, or the whole workgroup) hold K slots
 // each, thread t the slots t, t + threads, ...
 template <int IN, int K, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_ln_fwd(const NormFwd p) {
-  __shared__ float red[2][16];
-  __shared__ uint32_t redm[16];
+__global__ __launch_bounds__(WAVE ? 256 : 512) void k_ln_fwd(const NormFwd p) {
+  __shared__ float red[2][8];
+  __shared__ uint32_t redm[8];
   const int nt = WAVE ? 64 : blockDim.x;
-  const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
+  const int thread = WAVE ? threadIdx.x & 63 : threadIdx.x;
   const int per = WAVE ? kWaveRows : 1;
   const int nw = blockDim.x >> 6;
   const float n = (float)p.cols;
   const float ts = p.yq.scaling == kCastTensor ? *p.yq.scale : 1.0f;
   uint32_t amax = 0;
-  for (int64_t row = (int64_t)blockIdx.x * per + (WAVE ? threadIdx.x >> 6 : 0); row < p.rows;
+  const int own = WAVE ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) : 0;
+  for (int64_t row = (int64_t)blockIdx.x * per + own; row < p.rows;
        row += (int64_t)gridDim.x * per) {
+    const int t = afresh(thread);
     const uint8_t* xr =
         static_cast<const uint8_t*>(p.x) + row * p.cols * Slot<IN>::kBytes;
-    Slot<IN> x[K];
+    Slot<IN> raw[K];
+    float x[K][8];
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int slot = t + k * nt;
-      x[k].load(xr + (int64_t)slot * 8 * Slot<IN>::kBytes, p.cols - slot * 8);
+      raw[k].load(xr, slot * 8, p.cols);
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+      float s = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += x[k].get(i);
+      for (int i = 0; i < 8; ++i) s += x[k][i] = raw[k].get(i);
+      sum += s;
+    }
     const float mean = row_sum<WAVE>(sum, red[0], nw) / n;   // exact for a row of one value
     float sq = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int nv = p.cols - (t + k * nt) * 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float d = i < nv ? x[k].get(i) - mean : 0.0f;
-        sq += d * d;
+      for (int i = 0; i < 8; ++i) x[k][i] -= mean;
+      if (!__all(nv >= 8)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[k][i] = i < nv ? x[k][i] : 0.0f;
       }
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += x[k][i] * x[k][i];
+      sq += s;
     }
     const float var = row_sum<WAVE>(sq, red[1], nw) / n;
     const float rstd = 1.0f / sqrtf(var + p.eps);
@@ -98,15 +118,15 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_ln_fwd(const NormFwd p) {
       const int nv = p.cols - slot * 8;
       if (__all(nv <= 0)) continue;
       float h[8], y[8], g[8], b[8];
-      load_weight8(p.gamma, p.w_type, slot * 8, nv, g);
-      load_weight8(p.beta, p.w_type, slot * 8, nv, b);
+      load_weight8(p.gamma, p.w_type, slot * 8, p.cols, g);
+      load_weight8(p.beta, p.w_type, slot * 8, p.cols, b);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        h[i] = i < nv ? (x[k].get(i) - mean) * rstd : 0.0f;
+        h[i] = x[k][i] * rstd;
         y[i] = h[i] * g[i] + b[i];
       }
-      if (p.y && nv > 0) store_bf16x8(p.y + row * p.cols + (int64_t)slot * 8, y, nv);
-      if (p.xhat.q) cast_store(p.xhat, h, row, p.cols, slot, nv, 1.0f);
+      if (p.y && nv > 0) store_bf16x8(p.y + row * p.cols + (uint32_t)slot * 8, y, nv);
+      if (p.xhat.q) cast_store_tile(p.xhat, h, row, p.cols, slot, nv);
       if (p.yq.q) cast_store(p.yq, y, row, p.cols, slot, nv, ts);
       if (p.amax) amax = max(amax, absmax_f32x8(y));
     }
@@ -122,118 +142,199 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_ln_fwd(const NormFwd p) {
   }
 }
 
-// Backward.  Workgroup b walks the rows b, b + grid, ... (WAVE: kWaveRows
-// at a time) with its columns' sums of dy and dy xhat in registers, and
-// leaves them as row b of the partial sums: [dgamma | dbeta].
-template <int IN, bool HELD, int K, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_ln_bwd(const NormBwd p) {
+// Backward.  A workgroup holds `groups` rows at a time, each dealt to nt
+// threads with K slots a thread, and walks the tensor with its columns' sums
+// of dy and dy xhat in registers.  At the end its groups' sums are added up
+// in order and left as row b of the partial sums: [dgamma | dbeta].  A row
+// stays in registers as it was loaded, half the size of its widened values,
+// and is widened for the sums and again for dx, which makes room for the next
+// row's loads to go out before the present row is worked on.  K = 8 (rows
+// above 16384 columns) has room neither for those nor for gamma.
+template <int IN, bool HELD>
+struct BwdSlot {
+  Slot<kInBF16> d;
+  Slot<IN> x;        // !HELD
+  uint2 q;           // HELD
+  float s;
+  // `row` is the same in all lanes, so that addresses are a scalar base and
+  // a 32-bit offset
+  __device__ __forceinline__ void load(const NormBwd& p, int64_t row, int tiles, int slot) {
+    d.load(p.dy + row * p.cols, slot * 8, p.cols);
+    if constexpr (HELD) {
+      q = load_u8x8(p.xhat + row * p.cols, slot * 8, p.cols);
+      s = (p.xhat_scale + row * tiles)[(uint32_t)min(slot >> 4, tiles - 1)];
+    } else {
+      x.load(static_cast<const uint8_t*>(p.x) + row * p.cols * Slot<IN>::kBytes, slot * 8,
+             p.cols);
+    }
+  }
+  // Widen again afterwards, do not keep what has been widened so far.
+  __device__ __forceinline__ void forget() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(d.w[i]));
+    if constexpr (HELD) {
+      asm volatile("" : "+v"(q.x), "+v"(q.y));
+    } else {
+#pragma unroll
+      for (int i = 0; i < Slot<IN>::kWords; ++i) asm volatile("" : "+v"(x.w[i]));
+    }
+  }
+  // dy and xhat, zeros past the row's end
+  __device__ __forceinline__ void get(const NormBwd& p, float mean, float rstd, int nv,
+                                      float (&dy)[8], float (&h)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dy[i] = d.get(i);
+    if constexpr (HELD) {
+      decode8(p.xhat_fmt, q, s, h);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = (x.get(i) - mean) * rstd;
+      if (!__all(nv >= 8)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = i < nv ? h[i] : 0.0f;
+      }
+    }
+  }
+};
+
+// Threads of a workgroup: 1024 while 128 registers are enough.
+constexpr int bwd_threads(int k, bool held, int in) {
+  return k == 1 || (k == 2 && (held || in == kInBF16)) ? 1024 : 512;
+}
+template <int IN, bool HELD, int K>
+__global__ __launch_bounds__(bwd_threads(K, HELD, IN)) void k_ln_bwd(const NormBwd p, int nt,
+                                                               int groups) {
+  constexpr bool AHEAD = K <= 4;
   __shared__ float red[2][2][16];
-  const int nt = WAVE ? 64 : blockDim.x;
-  const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
-  const int per = WAVE ? kWaveRows : 1;
-  const int nw = blockDim.x >> 6;
-  const int64_t tiles = (p.cols + 127) >> 7;
+  extern __shared__ float sums[];            // [groups - 1][8][nt]
+  // a wave is of one group
+  const int group = __builtin_amdgcn_readfirstlane((int)threadIdx.x / nt);
+  const int thread = threadIdx.x - group * nt;
+  const int nw = nt >> 6, wave = thread >> 6, first = group * nw;
+  const int tiles = (p.cols + 127) >> 7;
   const float inv_n = 1.0f / (float)p.cols;
-  float g[K][8], dg[K][8], db[K][8];
+  const int64_t step = (int64_t)gridDim.x * groups;
+  float g[AHEAD ? K : 1][8], dg[K][8], db[K][8];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int slot = t + k * nt;
-    load_weight8(p.gamma, p.w_type, slot * 8, p.cols - slot * 8, g[k]);
+    const int slot = thread + k * nt;
+    if constexpr (AHEAD) load_weight8(p.gamma, p.w_type, slot * 8, p.cols, g[k]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dg[k][i] = db[k][i] = 0.0f;
   }
+  BwdSlot<IN, HELD> in[K], ahead[AHEAD ? K : 1];
+  float next_rstd = 0.0f, next_mean = 0.0f;
+  const auto fetch = [&](BwdSlot<IN, HELD> (&to)[K], int64_t row) {
+    if (row >= p.rows) return;               // the same for the whole wave
+    const int t = afresh(thread);
+    next_rstd = p.rstd[row];
+    next_mean = HELD ? 0.0f : p.mean[row];
+#pragma unroll
+    for (int k = 0; k < K; ++k) to[k].load(p, row, tiles, t + k * nt);
+  };
+  int64_t row = (int64_t)blockIdx.x * groups + group;
+  if constexpr (AHEAD) fetch(ahead, row);
   int flip = 0;
-  for (int64_t row = (int64_t)blockIdx.x * per + (WAVE ? threadIdx.x >> 6 : 0); row < p.rows;
-       row += (int64_t)gridDim.x * per, flip ^= 1) {
-    const float rstd = p.rstd[row];
-    const float mean = HELD ? 0.0f : p.mean[row];
-    float dy[K][8], h[K][8];
+  // the bound is the workgroup's first row, so that all groups meet its barriers
+  for (; row - group < p.rows; row += step, flip ^= 1) {
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) in[k] = ahead[k];
+    } else {
+      fetch(in, row);
+    }
+    const bool live = row < p.rows;
+    const float rstd = next_rstd, mean = next_mean;
+    if constexpr (AHEAD) fetch(ahead, row + step);
+    const int t = afresh(thread);
     float s1 = 0.0f, s2 = 0.0f;
+    if (live) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int slot = t + k * nt;
-      const int nv = p.cols - slot * 8;
-      Slot<kInBF16> d;
-      d.load(reinterpret_cast<const uint8_t*>(p.dy) + (row * p.cols + (int64_t)slot * 8) * 2, nv);
+      for (int k = 0; k < K; ++k) {
+        const int slot = t + k * nt;
+        auto& gk = g[AHEAD ? k : 0];
+        if constexpr (!AHEAD) load_weight8(p.gamma, p.w_type, slot * 8, p.cols, gk);
+        float dy[8], h[8];
+        in[k].get(p, mean, rstd, p.cols - slot * 8, dy, h);
+        float a1 = 0.0f, a2 = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dy[k][i] = d.get(i);
-      if constexpr (HELD) {
-        const float s = nv > 0 ? p.xhat_scale[row * tiles + (slot >> 4)] : 0.0f;
-        decode8(p.xhat_fmt, load_u8x8(p.xhat + row * p.cols + (int64_t)slot * 8, nv), s, h[k]);
-      } else {
-        Slot<IN> x;
-        x.load(static_cast<const uint8_t*>(p.x) +
-                   (row * p.cols + (int64_t)slot * 8) * Slot<IN>::kBytes, nv);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[k][i] = i < nv ? (x.get(i) - mean) * rstd : 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float gi = dy[k][i] * g[k][i];
-        s1 += gi;
-        s2 += gi * h[k][i];
-        dg[k][i] += dy[k][i] * h[k][i];
-        db[k][i] += dy[k][i];
+        for (int i = 0; i < 8; ++i) {
+          const float gi = dy[i] * gk[i];
+          a1 += gi;
+          a2 += gi * h[i];
+          dg[k][i] += dy[i] * h[i];
+          db[k][i] += dy[i];
+        }
+        s1 += a1;
+        s2 += a2;
+        __builtin_amdgcn_sched_barrier(0);   // one slot widened at a time
       }
     }
-    // two sets of LDS words, used in turn: one barrier a row
     s1 = wave_sum(s1);
     s2 = wave_sum(s2);
-    if constexpr (!WAVE) {
+    if (nw > 1) {
+      // two sets of LDS words, used in turn: one barrier a row
       if ((threadIdx.x & 63) == 0) {
-        red[flip][0][threadIdx.x >> 6] = s1;
-        red[flip][1][threadIdx.x >> 6] = s2;
+        red[flip][0][first + wave] = s1;
+        red[flip][1][first + wave] = s2;
       }
       __syncthreads();
       s1 = s2 = 0.0f;
       for (int i = 0; i < nw; ++i) {
-        s1 += red[flip][0][i];
-        s2 += red[flip][1][i];
+        s1 += red[flip][0][first + i];
+        s2 += red[flip][1][first + i];
       }
     }
     const float c1 = s1 * inv_n, c2 = s2 * inv_n;
+    if (live) {
+      const int u = afresh(thread);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int slot = u + k * nt;
+        const int nv = p.cols - slot * 8;
+        auto& gk = g[AHEAD ? k : 0];
+        if constexpr (!AHEAD) load_weight8(p.gamma, p.w_type, slot * 8, p.cols, gk);
+        if constexpr (!AHEAD) in[k].forget();
+        float dy[8], h[8], dx[8];
+        in[k].get(p, mean, rstd, nv, dy, h);
+        if (nv > 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dx[i] = rstd * (dy[i] * gk[i] - c1 - h[i] * c2);
+          const uint32_t at = (uint32_t)slot * 8;
+          if constexpr (IN == kInBF16)
+            store_bf16x8(static_cast<uint16_t*>(p.dx) + row * p.cols + at, dx, nv);
+          else
+            store_f32x8(static_cast<float*>(p.dx) + row * p.cols + at, dx, nv);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  if (groups > 1) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int slot = t + k * nt;
-      const int nv = p.cols - slot * 8;
-      if (nv <= 0) continue;
-      float dx[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dx[i] = rstd * (dy[k][i] * g[k][i] - c1 - h[k][i] * c2);
-      const int64_t at = row * p.cols + (int64_t)slot * 8;
-      if constexpr (IN == kInBF16) store_bf16x8(static_cast<uint16_t*>(p.dx) + at, dx, nv);
-      else store_f32x8(static_cast<float*>(p.dx) + at, dx, nv);
+      for (int half = 0; half < 2; ++half) {
+        auto& mine = half ? db[k] : dg[k];
+        __syncthreads();
+        if (group > 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sums[((group - 1) * 8 + i) * nt + thread] = mine[i];
+        }
+        __syncthreads();
+        if (group == 0) {
+          for (int o = 0; o < groups - 1; ++o)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mine[i] += sums[(o * 8 + i) * nt + thread];
+        }
+      }
     }
+    if (group > 0) return;
   }
   float* out = p.part + (int64_t)blockIdx.x * 2 * p.cols;
-  if constexpr (WAVE) {
-    // the workgroup's waves, one after the other
-    __shared__ float sums[2][K * 512];
-    for (int w = 0; w < nw; ++w) {
-      if ((int)(threadIdx.x >> 6) == w) {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int at = (i * K + k) * 64 + t;   // lanes side by side
-            sums[0][at] = w == 0 ? dg[k][i] : sums[0][at] + dg[k][i];
-            sums[1][at] = w == 0 ? db[k][i] : sums[1][at] + db[k][i];
-          }
-      }
-      __syncthreads();
-    }
-    if (threadIdx.x >= 64) return;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dg[k][i] = sums[0][(i * K + k) * 64 + t];
-        db[k][i] = sums[1][(i * K + k) * 64 + t];
-      }
-  }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int slot = t + k * nt;
+    const int slot = thread + k * nt;
     const int nv = p.cols - slot * 8;
     if (nv <= 0) continue;
     store_f32x8(out + slot * 8, dg[k], nv);
@@ -241,24 +342,25 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_ln_bwd(const NormBwd p) {
   }
 }
 
-// dgamma and dbeta from n rows of partial sums: 32 columns per workgroup,
-// 8 threads per column, in an order that does not depend on timing.
-__global__ __launch_bounds__(256) void k_ln_bwd_sum(const float* __restrict__ part, int n,
-                                                    int cols, float* __restrict__ dgamma,
-                                                    float* __restrict__ dbeta) {
-  __shared__ float red[8][32];
+// dgamma and dbeta from n rows of partial sums (at most 256): 32 columns per
+// workgroup, 32 threads per column, in an order that does not depend on
+// timing.
+__global__ __launch_bounds__(1024) void k_ln_bwd_sum(const float* __restrict__ part, int n,
+                                                     int cols, float* __restrict__ dgamma,
+                                                     float* __restrict__ dbeta) {
+  __shared__ float red[32][32];
   const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + c, width = 2 * (int64_t)cols;
   float s = 0.0f;
   if (col < width) {
-#pragma unroll 4
-    for (int i = g; i < n; i += 8) s += part[i * width + col];
+#pragma unroll 8
+    for (int i = g; i < n; i += 32) s += part[i * width + col];
   }
   red[g][c] = s;
   __syncthreads();
   if (g == 0 && col < width) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][c];
+    for (int i = 1; i < 32; ++i) s += red[i][c];
     if (col < cols) dgamma[col] = s;
     else dbeta[col - cols] = s;
   }
@@ -269,12 +371,29 @@ struct RowShape {
   int k, nt;
   bool wave;
 };
+int round_up64(int n) { return (n + 63) / 64 * 64; }
 RowShape row_shape(int64_t cols) {
   const int slots = (int)((cols + 7) / 8);
   if (slots <= 64) return {1, 64, true};
   if (slots <= 128) return {2, 64, true};
-  const int k = slots <= 256 ? 1 : slots <= 1024 ? 2 : 4;
-  return {k, ((slots + k - 1) / k + 63) / 64 * 64, false};
+  const int k = slots <= 256 ? 1 : slots <= 1024 ? 2 : slots <= 2048 ? 4 : 8;
+  return {k, round_up64((slots + k - 1) / k), false};
+}
+// The backward pass: `groups` rows of a workgroup at a time, as many as its
+// threads allow, fewer where all 256 CUs would not get a workgroup.
+struct BwdShape {
+  int k, nt, groups, grid;
+};
+BwdShape bwd_shape(int64_t rows, int64_t cols, bool held, int in) {
+  const int slots = (int)((cols + 7) / 8);
+  BwdShape b;
+  b.k = slots <= 64 ? 1 : slots <= 1024 ? 2 : slots <= 2048 ? 4 : 8;
+  b.nt = round_up64((slots + b.k - 1) / b.k);
+  const int64_t most = bwd_threads(b.k, held, in) / b.nt, even = (rows + 255) / 256;
+  b.groups = (int)(even < most ? (even > 1 ? even : 1) : most);
+  const int64_t need = (rows + b.groups - 1) / b.groups;
+  b.grid = (int)(need < 256 ? need : 256);
+  return b;
 }
 
 }  // namespace
@@ -295,7 +414,8 @@ hipError_t launch_layernorm_fwd(const NormFwd& p, hipStream_t s) {
     else if (r.wave) FP8SG_LN_FWD(IN, 2, true);         \
     else if (r.k == 1) FP8SG_LN_FWD(IN, 1, false);      \
     else if (r.k == 2) FP8SG_LN_FWD(IN, 2, false);      \
-    else FP8SG_LN_FWD(IN, 4, false);                    \
+    else if (r.k == 4) FP8SG_LN_FWD(IN, 4, false);      \
+    else FP8SG_LN_FWD(IN, 8, false);                    \
   } while (0)
   if (p.x_type == kInBF16) FP8SG_LN_FWD_IN(kInBF16);
   else FP8SG_LN_FWD_IN(kInF32);
@@ -304,28 +424,21 @@ hipError_t launch_layernorm_fwd(const NormFwd& p, hipStream_t s) {
   return launch_amax_finalize(p.part, g, p.amax, s);
 }
 
-int layernorm_bwd_partials(int64_t rows, int64_t cols) {
-  const RowShape r = row_shape(cols);
-  // a grid that a 256-CU device holds at once
-  const int64_t need = r.wave ? (rows + kWaveRows - 1) / kWaveRows : rows;
-  const int64_t cap = 256 * (r.wave ? 2 : r.nt <= 256 ? 4 : r.nt <= 512 ? 2 : 1);
-  return (int)(need < cap ? need : cap);
-}
+int layernorm_bwd_partials(int64_t rows) { return (int)(rows < 256 ? rows : 256); }
 
 hipError_t launch_layernorm_bwd(const NormBwd& p, hipStream_t s) {
-  const RowShape r = row_shape(p.cols);
-  const int g = layernorm_bwd_partials(p.rows, p.cols);
-  const int nt = r.wave ? 64 * kWaveRows : r.nt;
-  if (g > 0) {
-#define FP8SG_LN_BWD(IN, HELD, K, WAVE) \
-  hipLaunchKernelGGL((k_ln_bwd<IN, HELD, K, WAVE>), dim3(g), dim3(nt), 0, s, p)
-#define FP8SG_LN_BWD_IN(IN, HELD)                            \
-  do {                                                       \
-    if (r.wave && r.k == 1) FP8SG_LN_BWD(IN, HELD, 1, true);        \
-    else if (r.wave) FP8SG_LN_BWD(IN, HELD, 2, true);               \
-    else if (r.k == 1) FP8SG_LN_BWD(IN, HELD, 1, false);            \
-    else if (r.k == 2) FP8SG_LN_BWD(IN, HELD, 2, false);            \
-    else FP8SG_LN_BWD(IN, HELD, 4, false);                          \
+  const BwdShape b = bwd_shape(p.rows, p.cols, p.xhat != nullptr, p.x_type);
+  if (b.grid > 0) {
+    const unsigned lds = (unsigned)((b.groups - 1) * 8 * b.nt * sizeof(float));
+#define FP8SG_LN_BWD(IN, HELD, K)                                                        \
+  hipLaunchKernelGGL((k_ln_bwd<IN, HELD, K>), dim3(b.grid), dim3(b.nt * b.groups), lds, s, \
+                     p, b.nt, b.groups)
+#define FP8SG_LN_BWD_IN(IN, HELD)                \
+  do {                                           \
+    if (b.k == 1) FP8SG_LN_BWD(IN, HELD, 1);     \
+    else if (b.k == 2) FP8SG_LN_BWD(IN, HELD, 2); \
+    else if (b.k == 4) FP8SG_LN_BWD(IN, HELD, 4); \
+    else FP8SG_LN_BWD(IN, HELD, 8);              \
   } while (0)
     const bool held = p.xhat != nullptr;
     if (p.x_type == kInBF16) {
@@ -339,8 +452,8 @@ hipError_t launch_layernorm_bwd(const NormBwd& p, hipStream_t s) {
     if (err != hipSuccess) return err;
   }
   const int64_t width = 2 * (int64_t)p.cols;
-  hipLaunchKernelGGL(k_ln_bwd_sum, dim3((unsigned)((width + 31) / 32)), dim3(256), 0, s, p.part, g,
-                     p.cols, p.dgamma, p.dbeta);
+  hipLaunchKernelGGL(k_ln_bwd_sum, dim3((unsigned)((width + 31) / 32)), dim3(1024), 0, s, p.part,
+                     b.grid, p.cols, p.dgamma, p.dbeta);
   return hipGetLastError();
 }
 

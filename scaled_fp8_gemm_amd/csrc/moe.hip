@@ -222,7 +222,7 @@ __global__ __launch_bounds__(kThreads) void k_moe_dispatch(const MoeRows p, int6
     const int64_t left = p.cols - (int64_t)slot * 8;
     const int nv = left < 8 ? (int)left : 8;
     Slot<kInBF16> v;
-    v.load(reinterpret_cast<const uint8_t*>(x + w.row * p.cols + (int64_t)slot * 8), nv);
+    v.load(x + w.row * p.cols, (int64_t)slot * 8, p.cols);
     const int32_t* pos = p.pos + w.row * p.k;
     SlotCast c;
     if (xq.q) {
@@ -266,8 +266,8 @@ __global__ __launch_bounds__(kThreads) void k_moe_combine(const MoeRows p,
         const int64_t r = (uint32_t)p.pos[c];
         ok[j] = r < p.rows && j0 + j < p.k;
         wt[j] = weight ? weight[c] : 1.0f;
-        v[j].load(reinterpret_cast<const uint8_t*>(ys + (ok[j] ? r : 0) * p.cols + col),
-                  p.rows > 0 ? nv : 0);
+        if (p.rows > 0) v[j].load(ys + (ok[j] ? r : 0) * p.cols, col, p.cols);
+        else v[j].zero();
       }
 #pragma unroll
       for (int j = 0; j < KJ; ++j)
@@ -314,11 +314,12 @@ __global__ __launch_bounds__(kThreads) void k_moe_combine_bwd(
       const int64_t left = p.cols - col;
       const int nv = left < 8 ? (int)left : 8;
       Slot<kInBF16> d, v[KJ];
-      d.load(reinterpret_cast<const uint8_t*>(dy + tok * p.cols + col), nv);
+      d.load(dy + tok * p.cols, col, p.cols);
 #pragma unroll
-      for (int j = 0; j < KJ; ++j)
-        v[j].load(reinterpret_cast<const uint8_t*>(ys + row[j] * p.cols + col),
-                  p.rows > 0 ? nv : 0);
+      for (int j = 0; j < KJ; ++j) {
+        if (p.rows > 0) v[j].load(ys + row[j] * p.cols, col, p.cols);
+        else v[j].zero();
+      }
 #pragma unroll
       for (int j = 0; j < KJ; ++j) {
         if (!ok[j]) continue;

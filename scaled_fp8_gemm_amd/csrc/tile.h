@@ -6,9 +6,12 @@
 // then holds one 1x128 tile and a lane quad one 1x32 MX block, so a tile's
 // maximum is four DPP steps and an MX block's two, with no LDS.  Rows may
 // have any length: a slot's 8 elements move as one vector access at the
-// element's own alignment (global memory takes dwords at any address), and
-// the last slot of a row goes element by element.
+// element's own alignment (global memory takes dwords at any address); the
+// last slot of a row is read as the row's last 8 elements, the ones that
+// belong to the slot before dropped, and written element by element.
 #pragma once
+
+#include <type_traits>
 
 #include "fp8_device.h"
 #include "launch.h"
@@ -31,31 +34,91 @@ struct Slot {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = 0;
   }
-  // p: the slot's first element
-  __device__ __forceinline__ void load(const uint8_t* p, int nv) {
-    if (nv >= 8) {
-      if constexpr (IN == kInBF16) {
-        const u32x4_a2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
-        w[0] = v[0]; w[1] = v[1]; w[2] = v[2]; w[3] = v[3];
+  template <bool STREAM>
+  __device__ __forceinline__ void load8(const uint8_t* p) {
+    if constexpr (IN == kInBF16) {
+      const u32x4_a2* q = reinterpret_cast<const u32x4_a2*>(p);
+      u32x4_a2 v;
+      if constexpr (STREAM) v = __builtin_nontemporal_load(q);
+      else v = *q;
+      w[0] = v[0]; w[1] = v[1]; w[2] = v[2]; w[3] = v[3];
+    } else {
+      const u32x4_a4* q = reinterpret_cast<const u32x4_a4*>(p);
+      u32x4_a4 a, b;
+      if constexpr (STREAM) {
+        a = __builtin_nontemporal_load(q);
+        b = __builtin_nontemporal_load(q + 1);
       } else {
-        const u32x4_a4* q = reinterpret_cast<const u32x4_a4*>(p);
-        const u32x4_a4 a = __builtin_nontemporal_load(q), b = __builtin_nontemporal_load(q + 1);
-        w[0] = a[0]; w[1] = a[1]; w[2] = a[2]; w[3] = a[3];
-        w[4] = b[0]; w[5] = b[1]; w[6] = b[2]; w[7] = b[3];
+        a = q[0];
+        b = q[1];
       }
-      return;
+      w[0] = a[0]; w[1] = a[1]; w[2] = a[2]; w[3] = a[3];
+      w[4] = b[0]; w[5] = b[1]; w[6] = b[2]; w[7] = b[3];
     }
-    zero();
-    if (nv <= 0) return;
+  }
+  template <int N>
+  __device__ __forceinline__ void drop_words(bool yes) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i < nv) {
-        if constexpr (IN == kInBF16)
-          w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-        else
-          w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+    for (int i = 0; i < kWords; ++i) {
+      const uint32_t v = i + N < kWords ? w[(i + N) % kWords] : 0u;
+      w[i] = yes ? v : w[i];
+    }
+  }
+  // Drop the first s elements, zeros from the end.
+  __device__ __forceinline__ void drop(int s) {
+    if constexpr (IN == kInBF16) {
+      drop_words<2>(s & 4);
+      drop_words<1>(s & 2);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const uint32_t v = (w[i] >> 16) | (i + 1 < kWords ? w[(i + 1) % kWords] << 16 : 0u);
+        w[i] = (s & 1) ? v : w[i];
+      }
+    } else {
+      drop_words<4>(s & 4);
+      drop_words<2>(s & 2);
+      drop_words<1>(s & 1);
+    }
+    drop_words<kWords>(s >= 8);
+  }
+  // Columns col .. col + 7 of a row of `cols`: one vector load on every path
+  // but that of rows of fewer than 8.  A wave with lanes at or past the
+  // row's end moves theirs back to its last 8 elements and drops the front.
+  // STREAM: read once, otherwise read again.
+  template <bool STREAM, class I>
+  __device__ __forceinline__ void load_any(const uint8_t* row, I col, I cols) {
+    using U = std::make_unsigned_t<I>;
+    if (__all(cols - col >= 8)) {
+      load8<STREAM>(row + (U)col * kBytes);
+    } else if (cols >= 8) {
+      const I at = min(col, cols - 8);
+      load8<STREAM>(row + (U)at * kBytes);
+      drop((int)min(col - at, (I)8));
+    } else {
+      zero();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (col + i < cols) {
+          if constexpr (IN == kInBF16)
+            w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[(U)col + i]
+                        << (16 * (i & 1));
+          else
+            w[i] = reinterpret_cast<const uint32_t*>(row)[(U)col + i];
+        }
       }
     }
+  }
+  template <class I>
+  __device__ __forceinline__ void load(const uint8_t* row, I col, I cols) {
+    load_any<true>(row, col, cols);
+  }
+  template <class I>
+  __device__ __forceinline__ void load(const uint16_t* row, I col, I cols) {
+    load_any<true>(reinterpret_cast<const uint8_t*>(row), col, cols);
+  }
+  template <class I>
+  __device__ __forceinline__ void load_cached(const uint8_t* row, I col, I cols) {
+    load_any<false>(row, col, cols);
   }
   __device__ __forceinline__ float get(int i) const {
     if constexpr (IN == kInBF16)
@@ -116,19 +179,27 @@ __device__ __forceinline__ void store_u8x8(uint8_t* p, uint2 b, int nv) {
       if (i < nv) p[i] = (uint8_t)((i < 4 ? b.x : b.y) >> (8 * (i & 3)));
   }
 }
-__device__ __forceinline__ uint2 load_u8x8(const uint8_t* p, int nv) {
-  if (nv >= 8) {
-    const u32x2_a1 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_a1*>(p));
+// Bytes col .. col + 7 of a row of `cols`, as Slot's load.
+template <class I>
+__device__ __forceinline__ uint2 load_u8x8(const uint8_t* row, I col, I cols) {
+  using U = std::make_unsigned_t<I>;
+  if (__all(cols - col >= 8)) {
+    const u32x2_a1 v =
+        __builtin_nontemporal_load(reinterpret_cast<const u32x2_a1*>(row + (U)col));
     return make_uint2(v[0], v[1]);
   }
-  uint2 b = make_uint2(0, 0);
+  uint64_t b = 0;
+  if (cols >= 8) {
+    const I at = min(col, cols - 8);
+    const u32x2_a1 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_a1*>(row + (U)at));
+    const I s = col - at;
+    b = s >= 8 ? 0 : (((uint64_t)v[1] << 32) | v[0]) >> (8 * (int)(s & 7));
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < nv) {
-      if (i < 4) b.x |= (uint32_t)p[i] << (8 * i);
-      else b.y |= (uint32_t)p[i] << (8 * (i - 4));
-    }
-  return b;
+    for (int i = 0; i < 8; ++i)
+      if (col + i < cols) b |= (uint64_t)row[(U)col + i] << (8 * i);
+  }
+  return make_uint2((uint32_t)b, (uint32_t)(b >> 32));
 }
 
 // Eight FP8 bytes times s.
@@ -152,11 +223,14 @@ __device__ __forceinline__ void decode8(int fmt, uint2 b, float s, float (&v)[8]
   else decode8<kE5M2>(b, s, v);
 }
 
+// The largest magnitude's bits; a NaN among the values gives NaN's (the
+// maximum that keeps NaN, three operands an instruction, |.| free).
 __device__ __forceinline__ uint32_t absmax_f32x8(const float (&y)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
-  return m;
+  const auto top = [](float a, float b) {
+    return __builtin_elementwise_maximum(fabsf(a), fabsf(b));
+  };
+  const float a = top(top(y[0], y[1]), y[2]), b = top(top(y[3], y[4]), y[5]);
+  return __float_as_uint(top(top(top(a, b), y[6]), y[7]));
 }
 __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
   m = max(m, dpp<kDppXor1>(m));
@@ -168,49 +242,76 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t m) {
   return max(m, dpp<kDppRor8>(m));
 }
 
-// y * s -> eight FP8 bytes.  PLAIN: |y * s| <= fmax (1 + 2^-22) and no NaN,
-// so rounding alone ends at +-fmax and the converter needs no clamp.
-template <int FMT, bool PLAIN>
-__device__ __forceinline__ uint2 cast_f32x8(const float (&y)[8], float s) {
-  uint2 r;
-  if constexpr (PLAIN) {
-    int lo = 0, hi = 0;
-    if constexpr (FMT == kE4M3) {
-      lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] * s, y[1] * s, lo, false);
-      lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] * s, y[3] * s, lo, true);
-      hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4] * s, y[5] * s, hi, false);
-      hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6] * s, y[7] * s, hi, true);
-    } else {
-      lo = __builtin_amdgcn_cvt_pk_bf8_f32(y[0] * s, y[1] * s, lo, false);
-      lo = __builtin_amdgcn_cvt_pk_bf8_f32(y[2] * s, y[3] * s, lo, true);
-      hi = __builtin_amdgcn_cvt_pk_bf8_f32(y[4] * s, y[5] * s, hi, false);
-      hi = __builtin_amdgcn_cvt_pk_bf8_f32(y[6] * s, y[7] * s, hi, true);
-    }
-    r.x = (uint32_t)lo;
-    r.y = (uint32_t)hi;
-  } else {
-    r.x = cvt4<FMT>(y[0] * s, y[1] * s, y[2] * s, y[3] * s);
-    r.y = cvt4<FMT>(y[4] * s, y[5] * s, y[6] * s, y[7] * s);
-  }
-  return r;
-}
-
 constexpr uint32_t kInfBits = 0x7f800000u;
 
-// Scale of a 1x128 tile (m: its FP32 magnitude bits) and of a 1x32 MX block
-// (and its E8M0 byte): the rules of fp8_quantize_block and fp8_quantize_mx.
-template <int FMT>
-__device__ __forceinline__ float mx_scale_f32(uint32_t m, uint32_t& byte) {
-  int e = 0;
-  if (m >= kInfBits) {
-    byte = 0xffu;
-  } else if (m == 0u) {
-    byte = 127u;
-  } else {
-    e = mx_exponent_bits<FMT>(m);
-    byte = (uint32_t)(e + 127);
+// The formats' constants for a format known at run time (the same in all
+// lanes: scalar registers).
+__device__ __forceinline__ float fmax_of(int fmt) {
+  return fmt == kE4M3 ? FmtTraits<kE4M3>::fmax : FmtTraits<kE5M2>::fmax;
+}
+__device__ __forceinline__ int max_exp_of(int fmt) {
+  return fmt == kE4M3 ? FmtTraits<kE4M3>::max_exp : FmtTraits<kE5M2>::max_exp;
+}
+
+// y * s -> eight FP8 bytes.  clamp (wave-uniform): a value may be infinite,
+// NaN or above fmax (1 + 2^-22); otherwise rounding alone ends at +-fmax.
+__device__ __forceinline__ uint2 cast_f32x8(int fmt, const float (&y)[8], float s, bool clamp) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = y[i] * s;
+  if (clamp) {
+    const float m = fmax_of(fmt);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = __builtin_isnan(v[i]) ? v[i] : __builtin_amdgcn_fmed3f(v[i], -m, m);
   }
-  return __uint_as_float((uint32_t)(127 - e) << 23);
+  int lo = 0, hi = 0;
+  if (fmt == kE4M3) {
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], lo, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], hi, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
+  } else {
+    lo = __builtin_amdgcn_cvt_pk_bf8_f32(v[0], v[1], lo, false);
+    lo = __builtin_amdgcn_cvt_pk_bf8_f32(v[2], v[3], lo, true);
+    hi = __builtin_amdgcn_cvt_pk_bf8_f32(v[4], v[5], hi, false);
+    hi = __builtin_amdgcn_cvt_pk_bf8_f32(v[6], v[7], hi, true);
+  }
+  return make_uint2((uint32_t)lo, (uint32_t)hi);
+}
+
+// n / d rounded to nearest, for quotients and reciprocals far from FP32's
+// ends: a reciprocal refined once, and the quotient corrected by its exact
+// remainder.  (The general division also scales its operands and fixes up
+// special ones, about twice the instructions.)
+__device__ __forceinline__ float quotient(float n, float d) {
+  float r = __builtin_amdgcn_rcpf(d);
+  r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+  const float q = n * r;
+  return __builtin_fmaf(__builtin_fmaf(-d, q, n), r, q);
+}
+// Scale and scale_inv of a 1x128 tile (m: its magnitude bits), by the rule
+// of fp8_quantize_block: fmax / amax, 1 where amax is 0, infinite or NaN.
+__device__ __forceinline__ void tile_scale(int fmt, uint32_t m, float& s, float& inv) {
+  const float top = fmax_of(fmt);
+  const float a = m ? __uint_as_float(m) : top;
+  if (__all(a >= 0x1p-80f && a <= 0x1p100f)) {
+    s = quotient(top, a);
+    inv = quotient(1.0f, s);
+  } else {
+    s = fmt == kE4M3 ? scale_from_amax<kE4M3>(__uint_as_float(m))
+                     : scale_from_amax<kE5M2>(__uint_as_float(m));
+    inv = 1.0f / s;
+  }
+}
+// Scale of a 1x32 MX block and its E8M0 byte, by the rule of
+// fp8_quantize_mx.  The exponent's carry (mx_exponent_bits) comes from one
+// addition: fraction > 0x600000 overflows into the exponent field.
+__device__ __forceinline__ float mx_scale(int fmt, uint32_t m, uint32_t& byte) {
+  int b = max((int)((m + 0x1fffffu) >> 23) - max_exp_of(fmt), 0);
+  if (m - 1u >= kInfBits - 1u) b = 127;       // zero, infinite or NaN
+  byte = m >= kInfBits ? 0xffu : (uint32_t)b;
+  return __uint_as_float((uint32_t)(254 - b) << 23);
 }
 
 // A slot cast under `scaling`: its bytes, and its tile's or block's scale_inv
@@ -221,32 +322,30 @@ struct SlotCast {
   float scale_inv;
   uint32_t e8m0;
 };
-template <int FMT>
-__device__ __forceinline__ SlotCast cast_slot(int scaling, const float (&y)[8], float ts) {
+__device__ __forceinline__ SlotCast cast_slot(int scaling, int fmt, const float (&y)[8],
+                                              float ts) {
   SlotCast c;
   c.scale_inv = 1.0f;
   c.e8m0 = 127u;
-  if (scaling == kCastTensor) {
-    c.q = cast_f32x8<FMT, false>(y, ts);
-    return c;
-  }
   uint32_t m = absmax_f32x8(y);
-  float s;
-  if (scaling == kCastBlock) {
+  float s = ts;
+  bool big = false;
+  if (scaling == kCastTensor) {
+    big = !(__uint_as_float(m) * fabsf(ts) <= fmax_of(fmt));
+  } else if (scaling == kCastBlock) {
     m = row16_max(m);
-    s = scale_from_amax<FMT>(__uint_as_float(m));
-    c.scale_inv = 1.0f / s;
+    tile_scale(fmt, m, s, c.scale_inv);
+    big = m >= kInfBits;
   } else {
     m = quad_max(m);
-    s = mx_scale_f32<FMT>(m, c.e8m0);
+    s = mx_scale(fmt, m, c.e8m0);
+    big = m >= kInfBits;
   }
-  // wave-uniform: a tile with an infinity or NaN takes the clamping cast
-  if (__any(m >= kInfBits)) c.q = cast_f32x8<FMT, false>(y, s);
-  else c.q = cast_f32x8<FMT, true>(y, s);
+  c.q = cast_f32x8(fmt, y, s, __any(big));
   return c;
 }
 __device__ __forceinline__ SlotCast cast_slot(const CastOut& o, const float (&y)[8], float ts) {
-  return o.fmt == kE4M3 ? cast_slot<kE4M3>(o.scaling, y, ts) : cast_slot<kE5M2>(o.scaling, y, ts);
+  return cast_slot(o.scaling, o.fmt, y, ts);
 }
 // Its place in row `row` of an output of `cols` columns.
 __device__ __forceinline__ void store_cast(const CastOut& o, const SlotCast& c, int64_t row,
@@ -265,6 +364,15 @@ __device__ __forceinline__ void store_cast(const CastOut& o, const SlotCast& c, 
 __device__ __forceinline__ void cast_store(const CastOut& o, const float (&y)[8], int64_t row,
                                            int64_t cols, int slot, int nv, float ts) {
   store_cast(o, cast_slot(o, y, ts), row, cols, slot, nv);
+}
+// The same for an output known to have 1x128 tiles (a checkpoint).
+__device__ __forceinline__ void cast_store_tile(const CastOut& o, const float (&y)[8],
+                                                int64_t row, int64_t cols, int slot, int nv) {
+  const SlotCast c = cast_slot(kCastBlock, o.fmt, y, 1.0f);
+  if (nv <= 0) return;
+  store_u8x8(o.q + row * cols + (int64_t)slot * 8, c.q, nv);
+  if ((slot & 15) == 0)
+    static_cast<float*>(o.scale_inv)[row * ((cols + 127) >> 7) + (slot >> 4)] = c.scale_inv;
 }
 
 // Sums over the wave; every lane gets the result.
