@@ -372,8 +372,10 @@ struct RowShape {
   bool wave;
 };
 int round_up64(int n) { return (n + 63) / 64 * 64; }
-RowShape row_shape(int64_t cols) {
+RowShape row_shape(int64_t rows, int64_t cols) {
   const int slots = (int)((cols + 7) / 8);
+  // few rows: one slot a thread, for the shortest way through the row
+  if (rows <= 256 && slots > 64 && slots <= 512) return {1, round_up64(slots), false};
   if (slots <= 64) return {1, 64, true};
   if (slots <= 128) return {2, 64, true};
   const int k = slots <= 256 ? 1 : slots <= 1024 ? 2 : slots <= 2048 ? 4 : 8;
@@ -387,9 +389,12 @@ struct BwdShape {
 BwdShape bwd_shape(int64_t rows, int64_t cols, bool held, int in) {
   const int slots = (int)((cols + 7) / 8);
   BwdShape b;
-  b.k = slots <= 64 ? 1 : slots <= 1024 ? 2 : slots <= 2048 ? 4 : 8;
+  const int64_t even = (rows + 255) / 256;
+  // one slot a thread where all rows are in registers at once even so
+  b.k = slots <= 64 || even * round_up64(slots) <= 1024 ? 1 : slots <= 1024 ? 2
+        : slots <= 2048 ? 4 : 8;
   b.nt = round_up64((slots + b.k - 1) / b.k);
-  const int64_t most = bwd_threads(b.k, held, in) / b.nt, even = (rows + 255) / 256;
+  const int64_t most = bwd_threads(b.k, held, in) / b.nt;
   b.groups = (int)(even < most ? (even > 1 ? even : 1) : most);
   const int64_t need = (rows + b.groups - 1) / b.groups;
   b.grid = (int)(need < 256 ? need : 256);
@@ -401,7 +406,7 @@ BwdShape bwd_shape(int64_t rows, int64_t cols, bool held, int in) {
 hipError_t launch_layernorm_fwd(const NormFwd& p, hipStream_t s) {
   if (p.rows == 0)
     return p.amax ? launch_amax_finalize(p.part, 0, p.amax, s) : hipSuccess;
-  const RowShape r = row_shape(p.cols);
+  const RowShape r = row_shape(p.rows, p.cols);
   const int64_t need = r.wave ? (p.rows + kWaveRows - 1) / kWaveRows : p.rows;
   const int64_t cap = p.amax ? kMaxPartials : (int64_t)1 << 30;
   const int g = (int)(need < cap ? need : cap);

@@ -18,6 +18,7 @@ namespace fp8sg {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
 constexpr int kGroups = kThreads / 16;
 constexpr int kSortThreads = 1024;             // also the choices ranked at a time
 constexpr int kSortWaves = kSortThreads / 64;
@@ -38,9 +39,17 @@ __device__ __forceinline__ void count_choices(const int32_t* __restrict__ expert
                                               int64_t to, int experts, int columns,
                                               uint32_t* counters) {
   const int col = threadIdx.x & (columns - 1);
-  for (int64_t i = from + threadIdx.x; i < to; i += kSortThreads) {
-    const uint32_t e = (uint32_t)expert[i];
-    if (e < (uint32_t)experts) atomicAdd(&counters[e * columns + col], 1u);
+  constexpr int U = 8;                         // loads in flight
+  for (int64_t i = from + threadIdx.x; i < to; i += U * kSortThreads) {
+    uint32_t e[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t at = i + u * kSortThreads;
+      e[u] = at < to ? (uint32_t)expert[at] : 0xffffffffu;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (e[u] < (uint32_t)experts) atomicAdd(&counters[e[u] * columns + col], 1u);
   }
 }
 // Counters -> counts; every thread sums 8 counters of one expert.
@@ -189,8 +198,11 @@ __device__ __forceinline__ void zero_padding(const MoeRows& p, int64_t block, ui
   const int64_t end = min((int64_t)*p.end, p.rows);
   const float zero[8] = {};
   const int slots = (int)((p.cols + 7) >> 3);
-  for (int64_t r = block * kPadRows; r < min(end, (block + 1) * kPadRows); ++r) {
-    if (p.src[r] >= 0) continue;
+  const int64_t mine = block * kPadRows + (threadIdx.x & (kPadRows - 1));
+  // one load finds all of the workgroup's padding rows
+  uint32_t todo = (uint32_t)__ballot(mine < end && p.src[mine] < 0) & ((1u << kPadRows) - 1);
+  for (; todo; todo &= todo - 1) {
+    const int64_t r = block * kPadRows + __builtin_ctz(todo);
     for (int slot = threadIdx.x; slot < slots; slot += kThreads) {
       const int64_t left = p.cols - (int64_t)slot * 8;
       const int nv = left < 8 ? (int)left : 8;
@@ -206,36 +218,50 @@ __device__ __forceinline__ void zero_padding(const MoeRows& p, int64_t block, ui
   }
 }
 
+// A wave takes K slots a lane of a token's row, all loaded before the first
+// is cast; blockIdx.y walks the row's shares.
+template <int K>
 __global__ __launch_bounds__(kThreads) void k_moe_dispatch(const MoeRows p, int64_t token_blocks,
                                                            const uint16_t* __restrict__ x,
                                                            uint16_t* __restrict__ xs, CastOut xq) {
   if (blockIdx.x >= token_blocks) {
-    zero_padding(p, blockIdx.x - token_blocks, xs, xq);
+    if (blockIdx.y == 0) zero_padding(p, blockIdx.x - token_blocks, xs, xq);
     return;
   }
   const float ts = xq.scaling == kCastTensor ? *xq.scale : 1.0f;
-  const int lane = threadIdx.x & 15;
-  TileWalk w((int64_t)blockIdx.x * kGroups + (threadIdx.x >> 4), token_blocks * kGroups,
-             (int)((p.cols + 127) >> 7));
-  for (; w.row < p.tokens; w.next()) {
-    const int slot = w.tile * 16 + lane;
-    const int64_t left = p.cols - (int64_t)slot * 8;
-    const int nv = left < 8 ? (int)left : 8;
-    Slot<kInBF16> v;
-    v.load(x + w.row * p.cols, (int64_t)slot * 8, p.cols);
-    const int32_t* pos = p.pos + w.row * p.k;
-    SlotCast c;
-    if (xq.q) {
-      float f[8];
+  const int lane = threadIdx.x & 63;
+  const int64_t tok = (int64_t)blockIdx.x * kWaves +
+                      __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  if (tok >= p.tokens) return;
+  const int32_t* pos = p.pos + tok * p.k;
+  for (int64_t base = (int64_t)blockIdx.y * (K * 512); base < p.cols;
+       base += (int64_t)gridDim.y * (K * 512)) {
+    Slot<kInBF16> v[K];
+    SlotCast c[K];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = v.get(i);
-      c = cast_slot(xq, f, ts);
+    for (int i = 0; i < K; ++i)
+      if (base + i * 512 < p.cols) v[i].load(x + tok * p.cols, base + i * 512 + lane * 8, p.cols);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      if (base + i * 512 >= p.cols) break;
+      if (xq.q) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = v[i].get(e);
+        c[i] = cast_slot(xq, f, ts);
+      }
     }
     for (int j = 0; j < p.k; ++j) {
       const int64_t r = (uint32_t)pos[j];
       if (r >= p.rows) continue;
-      if (xs && nv > 0) store_slot(xs + r * p.cols + (int64_t)slot * 8, v, nv);
-      if (xq.q) store_cast(xq, c, r, p.cols, slot, nv);
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        const int64_t col = base + i * 512 + lane * 8;
+        const int64_t left = p.cols - col;
+        const int nv = left < 8 ? (int)left : 8;
+        if (xs && nv > 0) store_slot(xs + r * p.cols + col, v[i], nv);
+        if (xq.q) store_cast(xq, c[i], r, p.cols, (int)(col >> 3), nv);
+      }
     }
   }
 }
@@ -393,9 +419,18 @@ hipError_t launch_moe_sort(const int32_t* expert, int64_t n, int experts, int pa
 hipError_t launch_moe_dispatch(const MoeRows& p, const uint16_t* x, uint16_t* xs,
                                const CastOut& xq, hipStream_t s) {
   if (p.rows == 0 || p.cols == 0) return hipSuccess;
-  const int64_t tb = tile_blocks(p.tokens, p.cols);
-  hipLaunchKernelGGL(k_moe_dispatch, dim3((unsigned)(tb + pad_blocks(p.rows))), dim3(kThreads), 0,
-                     s, p, tb, x, xs, xq);
+  const int64_t tb = (p.tokens + kWaves - 1) / kWaves, gx = tb + pad_blocks(p.rows);
+  // as many waves as there are slots / 64 while the chip runs them at once
+  const int64_t shares = (p.cols + 511) / 512;
+  const int k = shares == 1 || p.tokens * shares <= 4096 ? 1 : shares == 2 ? 2 : 4;
+  const int64_t y = (shares + k - 1) / k;
+  const dim3 grid((unsigned)gx, (unsigned)(y < 65535 ? y : 65535));
+  if (k == 1)
+    hipLaunchKernelGGL(k_moe_dispatch<1>, grid, dim3(kThreads), 0, s, p, tb, x, xs, xq);
+  else if (k == 2)
+    hipLaunchKernelGGL(k_moe_dispatch<2>, grid, dim3(kThreads), 0, s, p, tb, x, xs, xq);
+  else
+    hipLaunchKernelGGL(k_moe_dispatch<4>, grid, dim3(kThreads), 0, s, p, tb, x, xs, xq);
   return hipGetLastError();
 }
 
