@@ -108,7 +108,11 @@ __global__ __launch_bounds__(kThreads) void k_act_fwd(const ActFwd p) {
     Slot<kInBF16> ha, hu;
     ha.load(hr, col, p.cols);
     if constexpr (GATED) hu.load(hr + p.cols, col, p.cols);
-    float a[8], u[8], y[8], q[8], d[8];
+    constexpr int H = GATED ? 2 : 1;
+    float h[H][8], out[1][8], q[8], d[8];
+    auto& a = h[0];
+    auto& u = h[H - 1];
+    auto& y = out[0];
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] = ha.get(i);
     act_slot<ACT, false>(a, q, d);
@@ -121,11 +125,13 @@ __global__ __launch_bounds__(kThreads) void k_act_fwd(const ActFwd p) {
       }
     }
     if (p.ckpt.q) {
-      cast_store_tile(p.ckpt, a, w.row * (GATED ? 2 : 1), p.cols, slot, nv);
-      if constexpr (GATED) cast_store_tile(p.ckpt, u, w.row * 2 + 1, p.cols, slot, nv);
+      SlotCast c[H];
+      cast_slots<H>(kCastBlock, p.ckpt.fmt, h, 1.0f, c);
+#pragma unroll
+      for (int i = 0; i < H; ++i) store_cast(p.ckpt, c[i], w.row * H + i, p.cols, slot, nv);
     }
     if (p.y && nv > 0) store_bf16x8(p.y + w.row * p.cols + col, y, nv);
-    if (p.yq.q) cast_store(p.yq, y, w.row, p.cols, slot, nv, ts);
+    if (p.yq.q) cast_store<false, 1>(p.yq, out, w.row, p.cols, slot, 0, ts);
     if (p.amax) amax = max(amax, absmax_f32x8(y));
   }
   if (p.amax) {
@@ -195,14 +201,12 @@ __global__ __launch_bounds__(kThreads) void k_ckpt_save(const uint16_t* __restri
              (int)((cols + 127) >> 7));
   for (; w.row < rows; w.next()) {
     const int slot = w.tile * 16 + lane;
-    const int64_t left = cols - (int64_t)slot * 8;
-    const int nv = left < 8 ? (int)left : 8;
     Slot<kInBF16> s;
     s.load(x + w.row * cols, (int64_t)slot * 8, cols);
-    float v[8];
+    float v[1][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = s.get(i);
-    cast_store_tile(o, v, w.row, cols, slot, nv);
+    for (int i = 0; i < 8; ++i) v[0][i] = s.get(i);
+    cast_store<true, 1>(o, v, w.row, cols, slot, 0, 1.0f);
   }
 }
 

@@ -57,9 +57,13 @@ __device__ __forceinline__ void load_weight8(const void* w, int type, int col, i
 }
 
 // Forward.  A row's threads (a wave, or the whole workgroup) hold K slots
-// each, thread t the slots t, t + threads, ...
+// each, thread t the slots t, t + threads, ...  Workgroups stay for several
+// rows with gamma and beta in registers, and the next row's loads go out
+// before the present row's sums.  K = 8 (rows above 16384 columns) has
+// registers for neither.
 template <int IN, int K, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : 512) void k_ln_fwd(const NormFwd p) {
+__global__ __launch_bounds__(WAVE ? 256 : 512, K == 3 && IN == kInBF16 ? 4 : 1) void k_ln_fwd(const NormFwd p) {
+  constexpr bool AHEAD = K <= 4;
   __shared__ float red[2][8];
   __shared__ uint32_t redm[8];
   const int nt = WAVE ? 64 : blockDim.x;
@@ -69,20 +73,31 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void k_ln_fwd(const NormFwd p) {
   const float n = (float)p.cols;
   const float ts = p.yq.scaling == kCastTensor ? *p.yq.scale : 1.0f;
   uint32_t amax = 0;
-  const int own = WAVE ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) : 0;
-  for (int64_t row = (int64_t)blockIdx.x * per + own; row < p.rows;
-       row += (int64_t)gridDim.x * per) {
+  Slot<IN> raw[K];
+  const auto fetch = [&](int64_t row) {
+    if (row >= p.rows) return;               // the same for the whole wave
     const int t = afresh(thread);
-    const uint8_t* xr =
-        static_cast<const uint8_t*>(p.x) + row * p.cols * Slot<IN>::kBytes;
-    Slot<IN> raw[K];
-    float x[K][8];
-    float sum = 0.0f;
+    const uint8_t* xr = static_cast<const uint8_t*>(p.x) + row * p.cols * Slot<IN>::kBytes;
+#pragma unroll
+    for (int k = 0; k < K; ++k) raw[k].load(xr, (t + k * nt) * 8, p.cols);
+  };
+  const int own = WAVE ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) : 0;
+  const int64_t step = (int64_t)gridDim.x * per;
+  int64_t row = (int64_t)blockIdx.x * per + own;
+  if constexpr (AHEAD) fetch(row);
+  float g[AHEAD ? K : 1][8], b[AHEAD ? K : 1][8];
+  if constexpr (AHEAD) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int slot = t + k * nt;
-      raw[k].load(xr, slot * 8, p.cols);
+      load_weight8(p.gamma, p.w_type, (thread + k * nt) * 8, p.cols, g[k]);
+      load_weight8(p.beta, p.w_type, (thread + k * nt) * 8, p.cols, b[k]);
     }
+  }
+  for (; row < p.rows; row += step) {
+    if constexpr (!AHEAD) fetch(row);
+    const int t = afresh(thread);
+    float x[K][8];
+    float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float s = 0.0f;
@@ -90,6 +105,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void k_ln_fwd(const NormFwd p) {
       for (int i = 0; i < 8; ++i) s += x[k][i] = raw[k].get(i);
       sum += s;
     }
+    if constexpr (AHEAD) fetch(row + step);
     const float mean = row_sum<WAVE>(sum, red[0], nw) / n;   // exact for a row of one value
     float sq = 0.0f;
 #pragma unroll
@@ -113,23 +129,33 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void k_ln_fwd(const NormFwd p) {
       p.rstd[row] = rstd;
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int slot = t + k * nt;
-      const int nv = p.cols - slot * 8;
-      if (__all(nv <= 0)) continue;
-      float h[8], y[8], g[8], b[8];
-      load_weight8(p.gamma, p.w_type, slot * 8, p.cols, g);
-      load_weight8(p.beta, p.w_type, slot * 8, p.cols, b);
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        h[i] = x[k][i] * rstd;
-        y[i] = h[i] * g[i] + b[i];
+      for (int i = 0; i < 8; ++i) x[k][i] *= rstd;
+    if (p.xhat.q) cast_store<true, K>(p.xhat, x, row, p.cols, t, nt, 1.0f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      auto& gk = g[AHEAD ? k : 0];
+      auto& bk = b[AHEAD ? k : 0];
+      if constexpr (!AHEAD) {
+        load_weight8(p.gamma, p.w_type, (t + k * nt) * 8, p.cols, gk);
+        load_weight8(p.beta, p.w_type, (t + k * nt) * 8, p.cols, bk);
       }
-      if (p.y && nv > 0) store_bf16x8(p.y + row * p.cols + (uint32_t)slot * 8, y, nv);
-      if (p.xhat.q) cast_store_tile(p.xhat, h, row, p.cols, slot, nv);
-      if (p.yq.q) cast_store(p.yq, y, row, p.cols, slot, nv, ts);
-      if (p.amax) amax = max(amax, absmax_f32x8(y));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[k][i] = x[k][i] * gk[i] + bk[i];
     }
+    if (p.y) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int slot = t + k * nt, nv = p.cols - slot * 8;
+        if (nv > 0) store_bf16x8(p.y + row * p.cols + (uint32_t)slot * 8, x[k], nv);
+      }
+    }
+    if (p.amax) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) amax = max(amax, absmax_f32x8(x[k]));
+    }
+    if (p.yq.q) cast_store<false, K>(p.yq, x, row, p.cols, t, nt, ts);
   }
   if (p.amax) {
     amax = wave_max_u32(amax);
@@ -150,17 +176,19 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void k_ln_fwd(const NormFwd p) {
 // and is widened for the sums and again for dx, which makes room for the next
 // row's loads to go out before the present row is worked on.  K = 8 (rows
 // above 16384 columns) has room neither for those nor for gamma.
-template <int IN, bool HELD>
+// HELD: the checkpoint's format, or kNotHeld.
+constexpr int kNotHeld = -1;
+template <int IN, int HELD>
 struct BwdSlot {
   Slot<kInBF16> d;
-  Slot<IN> x;        // !HELD
-  uint2 q;           // HELD
+  Slot<IN> x;        // without a checkpoint
+  uint2 q;           // with one
   float s;
   // `row` is the same in all lanes, so that addresses are a scalar base and
   // a 32-bit offset
   __device__ __forceinline__ void load(const NormBwd& p, int64_t row, int tiles, int slot) {
     d.load(p.dy + row * p.cols, slot * 8, p.cols);
-    if constexpr (HELD) {
+    if constexpr (HELD != kNotHeld) {
       q = load_u8x8(p.xhat + row * p.cols, slot * 8, p.cols);
       s = (p.xhat_scale + row * tiles)[(uint32_t)min(slot >> 4, tiles - 1)];
     } else {
@@ -172,20 +200,21 @@ struct BwdSlot {
   __device__ __forceinline__ void forget() {
 #pragma unroll
     for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(d.w[i]));
-    if constexpr (HELD) {
+    if constexpr (HELD != kNotHeld) {
       asm volatile("" : "+v"(q.x), "+v"(q.y));
     } else {
 #pragma unroll
       for (int i = 0; i < Slot<IN>::kWords; ++i) asm volatile("" : "+v"(x.w[i]));
     }
   }
-  // dy and xhat, zeros past the row's end
-  __device__ __forceinline__ void get(const NormBwd& p, float mean, float rstd, int nv,
-                                      float (&dy)[8], float (&h)[8]) const {
+  // dy and h, zeros past the row's end, with xhat = unit * h
+  __device__ __forceinline__ float get(const NormBwd& p, float mean, float rstd, int nv,
+                                       float (&dy)[8], float (&h)[8]) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) dy[i] = d.get(i);
-    if constexpr (HELD) {
-      decode8(p.xhat_fmt, q, s, h);
+    if constexpr (HELD != kNotHeld) {
+      widen8(HELD, q, h);
+      return s;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[i] = (x.get(i) - mean) * rstd;
@@ -193,6 +222,7 @@ struct BwdSlot {
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] = i < nv ? h[i] : 0.0f;
       }
+      return 1.0f;
     }
   }
 };
@@ -201,8 +231,8 @@ struct BwdSlot {
 constexpr int bwd_threads(int k, bool held, int in) {
   return k == 1 || (k == 2 && (held || in == kInBF16)) ? 1024 : 512;
 }
-template <int IN, bool HELD, int K>
-__global__ __launch_bounds__(bwd_threads(K, HELD, IN)) void k_ln_bwd(const NormBwd p, int nt,
+template <int IN, int HELD, int K>
+__global__ __launch_bounds__(bwd_threads(K, HELD != kNotHeld, IN)) void k_ln_bwd(const NormBwd p, int nt,
                                                                int groups) {
   constexpr bool AHEAD = K <= 4;
   __shared__ float red[2][2][16];
@@ -228,7 +258,7 @@ __global__ __launch_bounds__(bwd_threads(K, HELD, IN)) void k_ln_bwd(const NormB
     if (row >= p.rows) return;               // the same for the whole wave
     const int t = afresh(thread);
     next_rstd = p.rstd[row];
-    next_mean = HELD ? 0.0f : p.mean[row];
+    next_mean = HELD != kNotHeld ? 0.0f : p.mean[row];
 #pragma unroll
     for (int k = 0; k < K; ++k) to[k].load(p, row, tiles, t + k * nt);
   };
@@ -255,18 +285,18 @@ __global__ __launch_bounds__(bwd_threads(K, HELD, IN)) void k_ln_bwd(const NormB
         auto& gk = g[AHEAD ? k : 0];
         if constexpr (!AHEAD) load_weight8(p.gamma, p.w_type, slot * 8, p.cols, gk);
         float dy[8], h[8];
-        in[k].get(p, mean, rstd, p.cols - slot * 8, dy, h);
+        const float unit = in[k].get(p, mean, rstd, p.cols - slot * 8, dy, h);
         float a1 = 0.0f, a2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float gi = dy[i] * gk[i];
           a1 += gi;
           a2 += gi * h[i];
-          dg[k][i] += dy[i] * h[i];
+          dg[k][i] += dy[i] * (HELD != kNotHeld ? unit * h[i] : h[i]);
           db[k][i] += dy[i];
         }
         s1 += a1;
-        s2 += a2;
+        s2 += unit * a2;
         __builtin_amdgcn_sched_barrier(0);   // one slot widened at a time
       }
     }
@@ -285,7 +315,7 @@ __global__ __launch_bounds__(bwd_threads(K, HELD, IN)) void k_ln_bwd(const NormB
         s2 += red[flip][1][first + i];
       }
     }
-    const float c1 = s1 * inv_n, c2 = s2 * inv_n;
+    const float c1 = rstd * (s1 * inv_n), c2 = rstd * (s2 * inv_n);
     if (live) {
       const int u = afresh(thread);
 #pragma unroll
@@ -296,10 +326,10 @@ __global__ __launch_bounds__(bwd_threads(K, HELD, IN)) void k_ln_bwd(const NormB
         if constexpr (!AHEAD) load_weight8(p.gamma, p.w_type, slot * 8, p.cols, gk);
         if constexpr (!AHEAD) in[k].forget();
         float dy[8], h[8], dx[8];
-        in[k].get(p, mean, rstd, nv, dy, h);
+        const float c2h = c2 * in[k].get(p, mean, rstd, nv, dy, h);
         if (nv > 0) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dx[i] = rstd * (dy[i] * gk[i] - c1 - h[i] * c2);
+          for (int i = 0; i < 8; ++i) dx[i] = rstd * (dy[i] * gk[i]) - c1 - h[i] * c2h;
           const uint32_t at = (uint32_t)slot * 8;
           if constexpr (IN == kInBF16)
             store_bf16x8(static_cast<uint16_t*>(p.dx) + row * p.cols + at, dx, nv);
@@ -378,8 +408,9 @@ RowShape row_shape(int64_t rows, int64_t cols) {
   if (rows <= 256 && slots > 64 && slots <= 512) return {1, round_up64(slots), false};
   if (slots <= 64) return {1, 64, true};
   if (slots <= 128) return {2, 64, true};
-  const int k = slots <= 256 ? 1 : slots <= 1024 ? 2 : slots <= 2048 ? 4 : 8;
-  return {k, round_up64((slots + k - 1) / k), false};
+  // 4 or 8 waves, which spread evenly over a CU's SIMDs
+  const int nt = slots <= 768 ? 256 : 512, k = (slots + nt - 1) / nt;
+  return {k <= 4 ? k : 8, nt, false};
 }
 // The backward pass: `groups` rows of a workgroup at a time, as many as its
 // threads allow, fewer where all 256 CUs would not get a workgroup.
@@ -392,8 +423,8 @@ BwdShape bwd_shape(int64_t rows, int64_t cols, bool held, int in) {
   const int64_t even = (rows + 255) / 256;
   // one slot a thread where all rows are in registers at once even so
   b.k = slots <= 64 || even * round_up64(slots) <= 1024 ? 1 : slots <= 1024 ? 2
-        : slots <= 2048 ? 4 : 8;
-  b.nt = round_up64((slots + b.k - 1) / b.k);
+        : slots <= 1536 ? 3 : slots <= 2048 ? 4 : 8;
+  b.nt = b.k > 2 ? 512 : round_up64((slots + b.k - 1) / b.k);
   const int64_t most = bwd_threads(b.k, held, in) / b.nt;
   b.groups = (int)(even < most ? (even > 1 ? even : 1) : most);
   const int64_t need = (rows + b.groups - 1) / b.groups;
@@ -408,9 +439,13 @@ hipError_t launch_layernorm_fwd(const NormFwd& p, hipStream_t s) {
     return p.amax ? launch_amax_finalize(p.part, 0, p.amax, s) : hipSuccess;
   const RowShape r = row_shape(p.rows, p.cols);
   const int64_t need = r.wave ? (p.rows + kWaveRows - 1) / kWaveRows : p.rows;
-  const int64_t cap = p.amax ? kMaxPartials : (int64_t)1 << 30;
-  const int g = (int)(need < cap ? need : cap);
   const int nt = r.wave ? 64 * kWaveRows : r.nt;
+  // what a 256-CU device holds at once (by registers: 32, 16 or 8 waves a
+  // CU), rows dealt out evenly
+  const int waves = r.k == 1 ? 32 : r.k == 2 || (r.k == 3 && p.x_type == kInBF16) ? 16 : 8;
+  const int64_t held = 256 * (waves * 64 / nt), cap = held < kMaxPartials ? held : kMaxPartials;
+  const int64_t rounds = (need + cap - 1) / cap;
+  const int g = (int)((need + rounds - 1) / rounds);
 #define FP8SG_LN_FWD(IN, K, WAVE) \
   hipLaunchKernelGGL((k_ln_fwd<IN, K, WAVE>), dim3(g), dim3(nt), 0, s, p)
 #define FP8SG_LN_FWD_IN(IN)                      \
@@ -419,6 +454,7 @@ hipError_t launch_layernorm_fwd(const NormFwd& p, hipStream_t s) {
     else if (r.wave) FP8SG_LN_FWD(IN, 2, true);         \
     else if (r.k == 1) FP8SG_LN_FWD(IN, 1, false);      \
     else if (r.k == 2) FP8SG_LN_FWD(IN, 2, false);      \
+    else if (r.k == 3) FP8SG_LN_FWD(IN, 3, false);      \
     else if (r.k == 4) FP8SG_LN_FWD(IN, 4, false);      \
     else FP8SG_LN_FWD(IN, 8, false);                    \
   } while (0)
@@ -442,16 +478,19 @@ hipError_t launch_layernorm_bwd(const NormBwd& p, hipStream_t s) {
   do {                                           \
     if (b.k == 1) FP8SG_LN_BWD(IN, HELD, 1);     \
     else if (b.k == 2) FP8SG_LN_BWD(IN, HELD, 2); \
+    else if (b.k == 3) FP8SG_LN_BWD(IN, HELD, 3); \
     else if (b.k == 4) FP8SG_LN_BWD(IN, HELD, 4); \
     else FP8SG_LN_BWD(IN, HELD, 8);              \
   } while (0)
-    const bool held = p.xhat != nullptr;
+    const int held = p.xhat ? p.xhat_fmt : kNotHeld;
     if (p.x_type == kInBF16) {
-      if (held) FP8SG_LN_BWD_IN(kInBF16, true);
-      else FP8SG_LN_BWD_IN(kInBF16, false);
+      if (held == kE4M3) FP8SG_LN_BWD_IN(kInBF16, kE4M3);
+      else if (held == kE5M2) FP8SG_LN_BWD_IN(kInBF16, kE5M2);
+      else FP8SG_LN_BWD_IN(kInBF16, kNotHeld);
     } else {
-      if (held) FP8SG_LN_BWD_IN(kInF32, true);
-      else FP8SG_LN_BWD_IN(kInF32, false);
+      if (held == kE4M3) FP8SG_LN_BWD_IN(kInF32, kE4M3);
+      else if (held == kE5M2) FP8SG_LN_BWD_IN(kInF32, kE5M2);
+      else FP8SG_LN_BWD_IN(kInF32, kNotHeld);
     }
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;

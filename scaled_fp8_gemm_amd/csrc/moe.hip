@@ -210,8 +210,8 @@ __device__ __forceinline__ void zero_padding(const MoeRows& p, int64_t block, ui
       if (xq.q) {
         SlotCast c;
         c.q = make_uint2(0, 0);
-        c.scale_inv = 1.0f;
-        c.e8m0 = 127u;
+        if (xq.scaling == kCastMX) c.e8m0 = 127u;
+        else c.scale_inv = 1.0f;
         store_cast(xq, c, r, p.cols, slot, nv);
       }
     }
@@ -240,16 +240,14 @@ __global__ __launch_bounds__(kThreads) void k_moe_dispatch(const MoeRows p, int6
     SlotCast c[K];
 #pragma unroll
     for (int i = 0; i < K; ++i)
-      if (base + i * 512 < p.cols) v[i].load(x + tok * p.cols, base + i * 512 + lane * 8, p.cols);
+      v[i].load(x + tok * p.cols, base + i * 512 + lane * 8, p.cols);
+    if (xq.q) {
+      float f[K][8];
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-      if (base + i * 512 >= p.cols) break;
-      if (xq.q) {
-        float f[8];
+      for (int i = 0; i < K; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = v[i].get(e);
-        c[i] = cast_slot(xq, f, ts);
-      }
+        for (int e = 0; e < 8; ++e) f[i][e] = v[i].get(e);
+      cast_slots<K>(xq.scaling, xq.fmt, f, ts, c);
     }
     for (int j = 0; j < p.k; ++j) {
       const int64_t r = (uint32_t)pos[j];

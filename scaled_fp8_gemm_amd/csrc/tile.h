@@ -202,25 +202,27 @@ __device__ __forceinline__ uint2 load_u8x8(const uint8_t* row, I col, I cols) {
   return make_uint2((uint32_t)b, (uint32_t)(b >> 32));
 }
 
-// Eight FP8 bytes times s.
-template <int FMT>
-__device__ __forceinline__ void decode8(uint2 b, float s, float (&v)[8]) {
+// Eight FP8 bytes' values.
+__device__ __forceinline__ void widen8(int fmt, uint2 b, float (&v)[8]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int w = (int)(h ? b.y : b.x);
-    const auto lo = FMT == kE4M3 ? __builtin_amdgcn_cvt_pk_f32_fp8(w, false)
-                                 : __builtin_amdgcn_cvt_pk_f32_bf8(w, false);
-    const auto hi = FMT == kE4M3 ? __builtin_amdgcn_cvt_pk_f32_fp8(w, true)
-                                 : __builtin_amdgcn_cvt_pk_f32_bf8(w, true);
-    v[4 * h] = lo[0] * s;
-    v[4 * h + 1] = lo[1] * s;
-    v[4 * h + 2] = hi[0] * s;
-    v[4 * h + 3] = hi[1] * s;
+    if (fmt == kE4M3) {
+      const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
+      const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+      v[4 * h] = lo[0]; v[4 * h + 1] = lo[1]; v[4 * h + 2] = hi[0]; v[4 * h + 3] = hi[1];
+    } else {
+      const auto lo = __builtin_amdgcn_cvt_pk_f32_bf8(w, false);
+      const auto hi = __builtin_amdgcn_cvt_pk_f32_bf8(w, true);
+      v[4 * h] = lo[0]; v[4 * h + 1] = lo[1]; v[4 * h + 2] = hi[0]; v[4 * h + 3] = hi[1];
+    }
   }
 }
+// The same times s.
 __device__ __forceinline__ void decode8(int fmt, uint2 b, float s, float (&v)[8]) {
-  if (fmt == kE4M3) decode8<kE4M3>(b, s, v);
-  else decode8<kE5M2>(b, s, v);
+  widen8(fmt, b, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= s;
 }
 
 // The largest magnitude's bits; a NaN among the values gives NaN's (the
@@ -253,20 +255,11 @@ __device__ __forceinline__ int max_exp_of(int fmt) {
   return fmt == kE4M3 ? FmtTraits<kE4M3>::max_exp : FmtTraits<kE5M2>::max_exp;
 }
 
-// y * s -> eight FP8 bytes.  clamp (wave-uniform): a value may be infinite,
-// NaN or above fmax (1 + 2^-22); otherwise rounding alone ends at +-fmax.
-__device__ __forceinline__ uint2 cast_f32x8(int fmt, const float (&y)[8], float s, bool clamp) {
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = y[i] * s;
-  if (clamp) {
-    const float m = fmax_of(fmt);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i] = __builtin_isnan(v[i]) ? v[i] : __builtin_amdgcn_fmed3f(v[i], -m, m);
-  }
+// Eight scaled values -> eight FP8 bytes.
+template <int FMT>
+__device__ __forceinline__ uint2 narrow8(const float (&v)[8]) {
   int lo = 0, hi = 0;
-  if (fmt == kE4M3) {
+  if constexpr (FMT == kE4M3) {
     lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], lo, false);
     lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
     hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], hi, false);
@@ -290,18 +283,26 @@ __device__ __forceinline__ float quotient(float n, float d) {
   const float q = n * r;
   return __builtin_fmaf(__builtin_fmaf(-d, q, n), r, q);
 }
-// Scale and scale_inv of a 1x128 tile (m: its magnitude bits), by the rule
+// Scale and scale_inv of 1x128 tiles (m: their magnitude bits), by the rule
 // of fp8_quantize_block: fmax / amax, 1 where amax is 0, infinite or NaN.
-__device__ __forceinline__ void tile_scale(int fmt, uint32_t m, float& s, float& inv) {
+template <int K>
+__device__ __forceinline__ void tile_scales(int fmt, const uint32_t (&m)[K], float (&s)[K],
+                                            float (&inv)[K]) {
   const float top = fmax_of(fmt);
-  const float a = m ? __uint_as_float(m) : top;
-  if (__all(a >= 0x1p-80f && a <= 0x1p100f)) {
-    s = quotient(top, a);
-    inv = quotient(1.0f, s);
-  } else {
-    s = fmt == kE4M3 ? scale_from_amax<kE4M3>(__uint_as_float(m))
-                     : scale_from_amax<kE5M2>(__uint_as_float(m));
-    inv = 1.0f / s;
+  bool plain = true;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const float a = m[k] ? __uint_as_float(m[k]) : top;
+    plain = plain && a >= 0x1p-80f && a <= 0x1p100f;
+    s[k] = quotient(top, a);
+    inv[k] = quotient(1.0f, s[k]);
+  }
+  if (__all(plain)) return;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const float a = __uint_as_float(m[k]);
+    s[k] = fmt == kE4M3 ? scale_from_amax<kE4M3>(a) : scale_from_amax<kE5M2>(a);
+    inv[k] = 1.0f / s[k];
   }
 }
 // Scale of a 1x32 MX block and its E8M0 byte, by the rule of
@@ -314,38 +315,74 @@ __device__ __forceinline__ float mx_scale(int fmt, uint32_t m, uint32_t& byte) {
   return __uint_as_float((uint32_t)(254 - b) << 23);
 }
 
-// A slot cast under `scaling`: its bytes, and its tile's or block's scale_inv
-// or E8M0 byte.  All 16 lanes of a tile call it together, with zeros in y
-// past the row's end.  ts: the tensor's scale.
+// Slots cast under `scaling`: their bytes, and their tiles' or blocks'
+// scale_inv or E8M0 byte.  All 16 lanes of a tile call it together, with
+// zeros in y past the row's end.  ts: the tensor's scale.  A lane's K slots
+// go through each step side by side, so that their chains of dependent
+// instructions overlap and each choice is made once.
 struct SlotCast {
   uint2 q;
-  float scale_inv;
-  uint32_t e8m0;
+  union {
+    float scale_inv;
+    uint32_t e8m0;
+  };
 };
-__device__ __forceinline__ SlotCast cast_slot(int scaling, int fmt, const float (&y)[8],
-                                              float ts) {
-  SlotCast c;
-  c.scale_inv = 1.0f;
-  c.e8m0 = 127u;
-  uint32_t m = absmax_f32x8(y);
-  float s = ts;
+template <int K>
+__device__ __forceinline__ void cast_slots(int scaling, int fmt, const float (&y)[K][8], float ts,
+                                           SlotCast (&c)[K]) {
+  uint32_t m[K];
+  float s[K];
   bool big = false;
+#pragma unroll
+  for (int k = 0; k < K; ++k) m[k] = absmax_f32x8(y[k]);
   if (scaling == kCastTensor) {
-    big = !(__uint_as_float(m) * fabsf(ts) <= fmax_of(fmt));
-  } else if (scaling == kCastBlock) {
-    m = row16_max(m);
-    tile_scale(fmt, m, s, c.scale_inv);
-    big = m >= kInfBits;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      s[k] = ts;
+      big = big || !(__uint_as_float(m[k]) * fabsf(ts) <= fmax_of(fmt));
+    }
   } else {
-    m = quad_max(m);
-    s = mx_scale(fmt, m, c.e8m0);
-    big = m >= kInfBits;
+#pragma unroll
+    for (int k = 0; k < K; ++k) m[k] = quad_max(m[k]);
+    if (scaling == kCastBlock) {
+      float inv[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        m[k] = max(m[k], dpp<kDppRor4>(m[k]));
+        m[k] = max(m[k], dpp<kDppRor8>(m[k]));
+      }
+      tile_scales<K>(fmt, m, s, inv);
+#pragma unroll
+      for (int k = 0; k < K; ++k) c[k].scale_inv = inv[k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) s[k] = mx_scale(fmt, m[k], c[k].e8m0);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) big = big || m[k] >= kInfBits;
   }
-  c.q = cast_f32x8(fmt, y, s, __any(big));
-  return c;
-}
-__device__ __forceinline__ SlotCast cast_slot(const CastOut& o, const float (&y)[8], float ts) {
-  return cast_slot(o.scaling, o.fmt, y, ts);
+  float v[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[k][i] = y[k][i] * s[k];
+  // A wave with a value that may be infinite, NaN or above
+  // fmax (1 + 2^-22) clamps; otherwise rounding alone ends at +-fmax.
+  if (__any(big)) {
+    const float f = fmax_of(fmt);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[k][i] = __builtin_isnan(v[k][i]) ? v[k][i] : __builtin_amdgcn_fmed3f(v[k][i], -f, f);
+  }
+  if (fmt == kE4M3) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) c[k].q = narrow8<kE4M3>(v[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) c[k].q = narrow8<kE5M2>(v[k]);
+  }
 }
 // Its place in row `row` of an output of `cols` columns.
 __device__ __forceinline__ void store_cast(const CastOut& o, const SlotCast& c, int64_t row,
@@ -361,25 +398,36 @@ __device__ __forceinline__ void store_cast(const CastOut& o, const SlotCast& c, 
           (uint8_t)c.e8m0;
   }
 }
-__device__ __forceinline__ void cast_store(const CastOut& o, const float (&y)[8], int64_t row,
-                                           int64_t cols, int slot, int nv, float ts) {
-  store_cast(o, cast_slot(o, y, ts), row, cols, slot, nv);
-}
-// The same for an output known to have 1x128 tiles (a checkpoint).
-__device__ __forceinline__ void cast_store_tile(const CastOut& o, const float (&y)[8],
-                                                int64_t row, int64_t cols, int slot, int nv) {
-  const SlotCast c = cast_slot(kCastBlock, o.fmt, y, 1.0f);
-  if (nv <= 0) return;
-  store_u8x8(o.q + row * cols + (int64_t)slot * 8, c.q, nv);
-  if ((slot & 15) == 0)
-    static_cast<float*>(o.scale_inv)[row * ((cols + 127) >> 7) + (slot >> 4)] = c.scale_inv;
+// Slots first, first + step, ... of row `row`, cast and stored.  CHECKPOINT:
+// the output is known to have 1x128 tiles.
+template <bool CHECKPOINT, int K>
+__device__ __forceinline__ void cast_store(const CastOut& o, const float (&y)[K][8], int64_t row,
+                                           int64_t cols, int first, int step, float ts) {
+  SlotCast c[K];
+  cast_slots<K>(CHECKPOINT ? (int)kCastBlock : o.scaling, o.fmt, y, ts, c);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int slot = first + k * step;
+    const int64_t left = cols - (int64_t)slot * 8;
+    store_cast(o, c[k], row, cols, slot, left < 8 ? (int)left : 8);
+  }
 }
 
-// Sums over the wave; every lane gets the result.
+// Sum over the wave; every lane gets the result, the same bits.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+  const auto move = [](auto ctrl, float x) {
+    return __uint_as_float(dpp<decltype(ctrl)::value>(__float_as_uint(x)));
+  };
+  v += move(std::integral_constant<int, kDppXor1>{}, v);
+  v += move(std::integral_constant<int, kDppXor2>{}, v);
+  v += move(std::integral_constant<int, kDppRor4>{}, v);
+  v += move(std::integral_constant<int, kDppRor8>{}, v);
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                  false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                  false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 // A grid of 16-lane groups walking the (row, tile) pairs of a tensor of
