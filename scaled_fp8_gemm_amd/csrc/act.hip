@@ -91,7 +91,7 @@ __device__ __forceinline__ void act_slot(const float (&h)[8], float (&p)[8], flo
 }
 
 // One 16-lane group per (row, 128 columns) pair and step.
-template <int ACT, bool GATED>
+template <int ACT, bool GATED, bool TINY>
 __global__ __launch_bounds__(kThreads) void k_act_fwd(const ActFwd p) {
   __shared__ uint32_t red[kThreads / 64];
   const int lane = threadIdx.x & 15;
@@ -106,8 +106,10 @@ __global__ __launch_bounds__(kThreads) void k_act_fwd(const ActFwd p) {
     const int64_t col = (int64_t)slot * 8;
     const uint16_t* hr = p.h + w.row * p.cols * (GATED ? 2 : 1);
     Slot<kInBF16> ha, hu;
-    ha.load(hr, col, p.cols);
-    if constexpr (GATED) hu.load(hr + p.cols, col, p.cols);
+    ha.load<TINY>(hr, col, p.cols);
+    if constexpr (GATED) hu.load<TINY>(hr + p.cols, col, p.cols);
+    ha.settle<TINY>(col, p.cols);
+    if constexpr (GATED) hu.settle<TINY>(col, p.cols);
     constexpr int H = GATED ? 2 : 1;
     float h[H][8], out[1][8], q[8], d[8];
     auto& a = h[0];
@@ -140,7 +142,7 @@ __global__ __launch_bounds__(kThreads) void k_act_fwd(const ActFwd p) {
   }
 }
 
-template <int ACT, bool GATED, bool HELD>
+template <int ACT, bool GATED, bool HELD, bool TINY>
 __global__ __launch_bounds__(kThreads) void k_act_bwd(const ActBwd p) {
   const int lane = threadIdx.x & 15;
   const int tiles = (int)((p.cols + 127) >> 7);
@@ -153,27 +155,32 @@ __global__ __launch_bounds__(kThreads) void k_act_bwd(const ActBwd p) {
     if (nv <= 0) continue;
     const int64_t hrow = w.row * (GATED ? 2 : 1);
     Slot<kInBF16> g;
-    g.load(p.dy + w.row * p.cols, col, p.cols);
+    g.load<TINY>(p.dy + w.row * p.cols, col, p.cols);
     float a[8], u[8], y[8], da[8], du[8], q[8], d[8];
     if constexpr (HELD) {
       const uint8_t* held = p.ckpt + hrow * p.cols;
       const float* sc = p.ckpt_scale + hrow * tiles + w.tile;
-      const uint2 ba = load_u8x8(held, col, p.cols);
-      const uint2 bu = GATED ? load_u8x8(held + p.cols, col, p.cols) : make_uint2(0, 0);
+      uint2 ba = load_u8x8<TINY>(held, col, p.cols);
+      uint2 bu = GATED ? load_u8x8<TINY>(held + p.cols, col, p.cols) : make_uint2(0, 0);
       const float sa = sc[0], su = GATED ? sc[tiles] : 0.0f;
+      settle_u8x8<TINY>(ba, col, p.cols);
+      if constexpr (GATED) settle_u8x8<TINY>(bu, col, p.cols);
       decode8(p.ckpt_fmt, ba, sa, a);
       if constexpr (GATED) decode8(p.ckpt_fmt, bu, su, u);
     } else {
       const uint16_t* hr = p.h + hrow * p.cols;
       Slot<kInBF16> ha, hu;
-      ha.load(hr, col, p.cols);
-      if constexpr (GATED) hu.load(hr + p.cols, col, p.cols);
+      ha.load<TINY>(hr, col, p.cols);
+      if constexpr (GATED) hu.load<TINY>(hr + p.cols, col, p.cols);
+      ha.settle<TINY>(col, p.cols);
+      if constexpr (GATED) hu.settle<TINY>(col, p.cols);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         a[i] = ha.get(i);
         if constexpr (GATED) u[i] = hu.get(i);
       }
     }
+    g.settle<TINY>(col, p.cols);
     act_slot<ACT, true>(a, q, d);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -194,6 +201,7 @@ __global__ __launch_bounds__(kThreads) void k_act_bwd(const ActBwd p) {
 
 // A BF16 tensor into 1x128 tiles, rows of any length (fp8_quantize_block's
 // kernel, with 16-byte stores, takes whole tiles only).
+template <bool TINY>
 __global__ __launch_bounds__(kThreads) void k_ckpt_save(const uint16_t* __restrict__ x,
                                                         int64_t rows, int64_t cols, CastOut o) {
   const int lane = threadIdx.x & 15;
@@ -202,7 +210,8 @@ __global__ __launch_bounds__(kThreads) void k_ckpt_save(const uint16_t* __restri
   for (; w.row < rows; w.next()) {
     const int slot = w.tile * 16 + lane;
     Slot<kInBF16> s;
-    s.load(x + w.row * cols, (int64_t)slot * 8, cols);
+    s.load<TINY>(x + w.row * cols, (int64_t)slot * 8, cols);
+    s.settle<TINY>((int64_t)slot * 8, cols);
     float v[1][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[0][i] = s.get(i);
@@ -210,6 +219,7 @@ __global__ __launch_bounds__(kThreads) void k_ckpt_save(const uint16_t* __restri
   }
 }
 
+template <bool TINY>
 __global__ __launch_bounds__(kThreads) void k_ckpt_load(const uint8_t* __restrict__ q,
                                                         const float* __restrict__ scale_inv,
                                                         int fmt, int64_t rows, int64_t cols,
@@ -225,7 +235,10 @@ __global__ __launch_bounds__(kThreads) void k_ckpt_load(const uint8_t* __restric
     if (nv <= 0) continue;
     const int64_t at = w.row * cols + col;
     float v[8];
-    decode8(fmt, load_u8x8(q + w.row * cols, col, cols), scale_inv[w.row * tiles + w.tile], v);
+    uint2 b = load_u8x8<TINY>(q + w.row * cols, col, cols);
+    const float s = scale_inv[w.row * tiles + w.tile];
+    settle_u8x8<TINY>(b, col, cols);
+    decode8(fmt, b, s, v);
     store_bf16x8(y + at, v, nv);
   }
 }
@@ -259,8 +272,12 @@ hipError_t launch_act_fwd(const ActFwd& p, hipStream_t s) {
   if (p.rows * p.cols == 0)
     return p.amax ? launch_amax_finalize(p.part, 0, p.amax, s) : hipSuccess;
   const int g = tile_grid(p.rows, p.cols, p.amax ? kMaxPartials : kAnyGrid);
-  FP8SG_ACT_DISPATCH(p.act, p.gated,
-                     hipLaunchKernelGGL((k_act_fwd<A, G>), dim3(g), dim3(kThreads), 0, s, p));
+  FP8SG_ACT_DISPATCH(p.act, p.gated, {
+    if (p.cols < 8)
+      hipLaunchKernelGGL((k_act_fwd<A, G, true>), dim3(g), dim3(kThreads), 0, s, p);
+    else
+      hipLaunchKernelGGL((k_act_fwd<A, G, false>), dim3(g), dim3(kThreads), 0, s, p);
+  });
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || !p.amax) return err;
   return launch_amax_finalize(p.part, g, p.amax, s);
@@ -270,10 +287,14 @@ hipError_t launch_act_bwd(const ActBwd& p, hipStream_t s) {
   if (p.rows * p.cols == 0) return hipSuccess;
   const int g = tile_grid(p.rows, p.cols, kAnyGrid);
   FP8SG_ACT_DISPATCH(p.act, p.gated, {
-    if (p.ckpt)
-      hipLaunchKernelGGL((k_act_bwd<A, G, true>), dim3(g), dim3(kThreads), 0, s, p);
+    if (p.cols < 8 && p.ckpt)
+      hipLaunchKernelGGL((k_act_bwd<A, G, true, true>), dim3(g), dim3(kThreads), 0, s, p);
+    else if (p.cols < 8)
+      hipLaunchKernelGGL((k_act_bwd<A, G, false, true>), dim3(g), dim3(kThreads), 0, s, p);
+    else if (p.ckpt)
+      hipLaunchKernelGGL((k_act_bwd<A, G, true, false>), dim3(g), dim3(kThreads), 0, s, p);
     else
-      hipLaunchKernelGGL((k_act_bwd<A, G, false>), dim3(g), dim3(kThreads), 0, s, p);
+      hipLaunchKernelGGL((k_act_bwd<A, G, false, false>), dim3(g), dim3(kThreads), 0, s, p);
   });
   return hipGetLastError();
 }
@@ -283,16 +304,24 @@ hipError_t launch_checkpoint_save(const uint16_t* x, int64_t rows, int64_t cols,
   if (rows * cols == 0) return hipSuccess;
   if (cols % 128 == 0)
     return launch_quantize_block(x, rows, cols, o.fmt, 1, o.q, static_cast<float*>(o.scale_inv), s);
-  hipLaunchKernelGGL(k_ckpt_save, dim3(tile_grid(rows, cols, kAnyGrid)), dim3(kThreads), 0, s, x,
-                     rows, cols, o);
+  const dim3 g(tile_grid(rows, cols, kAnyGrid));
+  if (cols < 8)
+    hipLaunchKernelGGL(k_ckpt_save<true>, g, dim3(kThreads), 0, s, x, rows, cols, o);
+  else
+    hipLaunchKernelGGL(k_ckpt_save<false>, g, dim3(kThreads), 0, s, x, rows, cols, o);
   return hipGetLastError();
 }
 
 hipError_t launch_checkpoint_load(const uint8_t* q, const float* scale_inv, int fmt, int64_t rows,
                                   int64_t cols, uint16_t* y, hipStream_t s) {
   if (rows * cols == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_ckpt_load, dim3(tile_grid(rows, cols, kAnyGrid)), dim3(kThreads), 0, s, q,
-                     scale_inv, fmt, rows, cols, y);
+  const dim3 g(tile_grid(rows, cols, kAnyGrid));
+  if (cols < 8)
+    hipLaunchKernelGGL(k_ckpt_load<true>, g, dim3(kThreads), 0, s, q, scale_inv, fmt, rows, cols,
+                       y);
+  else
+    hipLaunchKernelGGL(k_ckpt_load<false>, g, dim3(kThreads), 0, s, q, scale_inv, fmt, rows, cols,
+                       y);
   return hipGetLastError();
 }
 

@@ -41,16 +41,19 @@ __device__ __forceinline__ int afresh(int t) {
 
 // gamma / beta of a slot: BF16 or FP32, widened.  Every row reads them
 // again, so they stay in the caches (no streaming loads).
+template <bool TINY>
 __device__ __forceinline__ void load_weight8(const void* w, int type, int col, int cols,
                                              float (&v)[8]) {
   if (type == kInBF16) {
     Slot<kInBF16> s;
-    s.load_cached(static_cast<const uint8_t*>(w), col, cols);
+    s.load_cached<TINY>(static_cast<const uint8_t*>(w), col, cols);
+    s.settle<TINY>(col, cols);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = s.get(i);
   } else {
     Slot<kInF32> s;
-    s.load_cached(static_cast<const uint8_t*>(w), col, cols);
+    s.load_cached<TINY>(static_cast<const uint8_t*>(w), col, cols);
+    s.settle<TINY>(col, cols);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = s.get(i);
   }
@@ -61,11 +64,16 @@ __device__ __forceinline__ void load_weight8(const void* w, int type, int col, i
 // rows with gamma and beta in registers, and the next row's loads go out
 // before the present row's sums.  K = 8 (rows above 16384 columns) has
 // registers for neither.
-template <int IN, int K, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : 512, K == 3 && IN == kInBF16 ? 4 : 1) void k_ln_fwd(const NormFwd p) {
-  constexpr bool AHEAD = K <= 4;
-  __shared__ float red[2][8];
-  __shared__ uint32_t redm[8];
+// Waves of a CU by registers:
+constexpr int fwd_waves(int k, int in) {
+  return k == 1 ? 32 : k == 2 || (k == 3 && in == kInBF16) ? 16 : 8;
+}
+template <int IN, int K, bool WAVE, bool TINY>
+__global__ __launch_bounds__(WAVE ? 256 : K == 2 ? 1024 : 512, fwd_waves(K, IN) / 4) void k_ln_fwd(
+    const NormFwd p) {
+  constexpr bool AHEAD = K <= 3;
+  __shared__ float red[2][16];
+  __shared__ uint32_t redm[16];
   const int nt = WAVE ? 64 : blockDim.x;
   const int thread = WAVE ? threadIdx.x & 63 : threadIdx.x;
   const int per = WAVE ? kWaveRows : 1;
@@ -79,7 +87,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 512, K == 3 && IN == kInBF16 ? 4 : 1) 
     const int t = afresh(thread);
     const uint8_t* xr = static_cast<const uint8_t*>(p.x) + row * p.cols * Slot<IN>::kBytes;
 #pragma unroll
-    for (int k = 0; k < K; ++k) raw[k].load(xr, (t + k * nt) * 8, p.cols);
+    for (int k = 0; k < K; ++k) raw[k].template load<TINY>(xr, (t + k * nt) * 8, p.cols);
   };
   const int own = WAVE ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) : 0;
   const int64_t step = (int64_t)gridDim.x * per;
@@ -89,8 +97,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 512, K == 3 && IN == kInBF16 ? 4 : 1) 
   if constexpr (AHEAD) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      load_weight8(p.gamma, p.w_type, (thread + k * nt) * 8, p.cols, g[k]);
-      load_weight8(p.beta, p.w_type, (thread + k * nt) * 8, p.cols, b[k]);
+      load_weight8<TINY>(p.gamma, p.w_type, (thread + k * nt) * 8, p.cols, g[k]);
+      load_weight8<TINY>(p.beta, p.w_type, (thread + k * nt) * 8, p.cols, b[k]);
     }
   }
   for (; row < p.rows; row += step) {
@@ -100,6 +108,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 512, K == 3 && IN == kInBF16 ? 4 : 1) 
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+      raw[k].template settle<TINY>((t + k * nt) * 8, p.cols);
       float s = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) s += x[k][i] = raw[k].get(i);
@@ -138,8 +147,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 512, K == 3 && IN == kInBF16 ? 4 : 1) 
       auto& gk = g[AHEAD ? k : 0];
       auto& bk = b[AHEAD ? k : 0];
       if constexpr (!AHEAD) {
-        load_weight8(p.gamma, p.w_type, (t + k * nt) * 8, p.cols, gk);
-        load_weight8(p.beta, p.w_type, (t + k * nt) * 8, p.cols, bk);
+        load_weight8<TINY>(p.gamma, p.w_type, (t + k * nt) * 8, p.cols, gk);
+        load_weight8<TINY>(p.beta, p.w_type, (t + k * nt) * 8, p.cols, bk);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[k][i] = x[k][i] * gk[i] + bk[i];
@@ -178,7 +187,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 512, K == 3 && IN == kInBF16 ? 4 : 1) 
 // above 16384 columns) has room neither for those nor for gamma.
 // HELD: the checkpoint's format, or kNotHeld.
 constexpr int kNotHeld = -1;
-template <int IN, int HELD>
+template <int IN, int HELD, bool TINY>
 struct BwdSlot {
   Slot<kInBF16> d;
   Slot<IN> x;        // without a checkpoint
@@ -187,14 +196,19 @@ struct BwdSlot {
   // `row` is the same in all lanes, so that addresses are a scalar base and
   // a 32-bit offset
   __device__ __forceinline__ void load(const NormBwd& p, int64_t row, int tiles, int slot) {
-    d.load(p.dy + row * p.cols, slot * 8, p.cols);
+    d.template load<TINY>(p.dy + row * p.cols, slot * 8, p.cols);
     if constexpr (HELD != kNotHeld) {
-      q = load_u8x8(p.xhat + row * p.cols, slot * 8, p.cols);
+      q = load_u8x8<TINY>(p.xhat + row * p.cols, slot * 8, p.cols);
       s = (p.xhat_scale + row * tiles)[(uint32_t)min(slot >> 4, tiles - 1)];
     } else {
-      x.load(static_cast<const uint8_t*>(p.x) + row * p.cols * Slot<IN>::kBytes, slot * 8,
-             p.cols);
+      x.template load<TINY>(static_cast<const uint8_t*>(p.x) + row * p.cols * Slot<IN>::kBytes,
+                            slot * 8, p.cols);
     }
+  }
+  __device__ __forceinline__ void settle(int slot, int cols) {
+    d.template settle<TINY>(slot * 8, cols);
+    if constexpr (HELD != kNotHeld) settle_u8x8<TINY>(q, slot * 8, cols);
+    else x.template settle<TINY>(slot * 8, cols);
   }
   // Widen again afterwards, do not keep what has been widened so far.
   __device__ __forceinline__ void forget() {
@@ -231,7 +245,7 @@ struct BwdSlot {
 constexpr int bwd_threads(int k, bool held, int in) {
   return k == 1 || (k == 2 && (held || in == kInBF16)) ? 1024 : 512;
 }
-template <int IN, int HELD, int K>
+template <int IN, int HELD, int K, bool TINY>
 __global__ __launch_bounds__(bwd_threads(K, HELD != kNotHeld, IN)) void k_ln_bwd(const NormBwd p, int nt,
                                                                int groups) {
   constexpr bool AHEAD = K <= 4;
@@ -248,13 +262,13 @@ __global__ __launch_bounds__(bwd_threads(K, HELD != kNotHeld, IN)) void k_ln_bwd
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int slot = thread + k * nt;
-    if constexpr (AHEAD) load_weight8(p.gamma, p.w_type, slot * 8, p.cols, g[k]);
+    if constexpr (AHEAD) load_weight8<TINY>(p.gamma, p.w_type, slot * 8, p.cols, g[k]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dg[k][i] = db[k][i] = 0.0f;
   }
-  BwdSlot<IN, HELD> in[K], ahead[AHEAD ? K : 1];
+  BwdSlot<IN, HELD, TINY> in[K], ahead[AHEAD ? K : 1];
   float next_rstd = 0.0f, next_mean = 0.0f;
-  const auto fetch = [&](BwdSlot<IN, HELD> (&to)[K], int64_t row) {
+  const auto fetch = [&](BwdSlot<IN, HELD, TINY> (&to)[K], int64_t row) {
     if (row >= p.rows) return;               // the same for the whole wave
     const int t = afresh(thread);
     next_rstd = p.rstd[row];
@@ -283,8 +297,9 @@ __global__ __launch_bounds__(bwd_threads(K, HELD != kNotHeld, IN)) void k_ln_bwd
       for (int k = 0; k < K; ++k) {
         const int slot = t + k * nt;
         auto& gk = g[AHEAD ? k : 0];
-        if constexpr (!AHEAD) load_weight8(p.gamma, p.w_type, slot * 8, p.cols, gk);
+        if constexpr (!AHEAD) load_weight8<TINY>(p.gamma, p.w_type, slot * 8, p.cols, gk);
         float dy[8], h[8];
+        in[k].settle(slot, p.cols);
         const float unit = in[k].get(p, mean, rstd, p.cols - slot * 8, dy, h);
         float a1 = 0.0f, a2 = 0.0f;
 #pragma unroll
@@ -323,7 +338,7 @@ __global__ __launch_bounds__(bwd_threads(K, HELD != kNotHeld, IN)) void k_ln_bwd
         const int slot = u + k * nt;
         const int nv = p.cols - slot * 8;
         auto& gk = g[AHEAD ? k : 0];
-        if constexpr (!AHEAD) load_weight8(p.gamma, p.w_type, slot * 8, p.cols, gk);
+        if constexpr (!AHEAD) load_weight8<TINY>(p.gamma, p.w_type, slot * 8, p.cols, gk);
         if constexpr (!AHEAD) in[k].forget();
         float dy[8], h[8], dx[8];
         const float c2h = c2 * in[k].get(p, mean, rstd, nv, dy, h);
@@ -408,9 +423,11 @@ RowShape row_shape(int64_t rows, int64_t cols) {
   if (rows <= 256 && slots > 64 && slots <= 512) return {1, round_up64(slots), false};
   if (slots <= 64) return {1, 64, true};
   if (slots <= 128) return {2, 64, true};
-  // 4 or 8 waves, which spread evenly over a CU's SIMDs
-  const int nt = slots <= 768 ? 256 : 512, k = (slots + nt - 1) / nt;
-  return {k <= 4 ? k : 8, nt, false};
+  // 4, 8 or 16 waves, which spread evenly over a CU's SIMDs
+  if (slots <= 768) return {(slots + 255) / 256, 256, false};
+  if (slots <= 1536) return {(slots + 511) / 512, 512, false};
+  if (slots <= 2048) return {2, 1024, false};
+  return {8, 512, false};
 }
 // The backward pass: `groups` rows of a workgroup at a time, as many as its
 // threads allow, fewer where all 256 CUs would not get a workgroup.
@@ -440,23 +457,21 @@ hipError_t launch_layernorm_fwd(const NormFwd& p, hipStream_t s) {
   const RowShape r = row_shape(p.rows, p.cols);
   const int64_t need = r.wave ? (p.rows + kWaveRows - 1) / kWaveRows : p.rows;
   const int nt = r.wave ? 64 * kWaveRows : r.nt;
-  // what a 256-CU device holds at once (by registers: 32, 16 or 8 waves a
-  // CU), rows dealt out evenly
-  const int waves = r.k == 1 ? 32 : r.k == 2 || (r.k == 3 && p.x_type == kInBF16) ? 16 : 8;
-  const int64_t held = 256 * (waves * 64 / nt), cap = held < kMaxPartials ? held : kMaxPartials;
+  // what a 256-CU device holds at once, rows dealt out evenly
+  const int64_t held = 256 * (fwd_waves(r.k, p.x_type) * 64 / nt), cap = held < kMaxPartials ? held : kMaxPartials;
   const int64_t rounds = (need + cap - 1) / cap;
   const int g = (int)((need + rounds - 1) / rounds);
-#define FP8SG_LN_FWD(IN, K, WAVE) \
-  hipLaunchKernelGGL((k_ln_fwd<IN, K, WAVE>), dim3(g), dim3(nt), 0, s, p)
-#define FP8SG_LN_FWD_IN(IN)                      \
-  do {                                           \
-    if (r.wave && r.k == 1) FP8SG_LN_FWD(IN, 1, true);  \
-    else if (r.wave) FP8SG_LN_FWD(IN, 2, true);         \
-    else if (r.k == 1) FP8SG_LN_FWD(IN, 1, false);      \
-    else if (r.k == 2) FP8SG_LN_FWD(IN, 2, false);      \
-    else if (r.k == 3) FP8SG_LN_FWD(IN, 3, false);      \
-    else if (r.k == 4) FP8SG_LN_FWD(IN, 4, false);      \
-    else FP8SG_LN_FWD(IN, 8, false);                    \
+#define FP8SG_LN_FWD(IN, K, WAVE, TINY) \
+  hipLaunchKernelGGL((k_ln_fwd<IN, K, WAVE, TINY>), dim3(g), dim3(nt), 0, s, p)
+#define FP8SG_LN_FWD_IN(IN)                                     \
+  do {                                                          \
+    if (p.cols < 8) FP8SG_LN_FWD(IN, 1, true, true);            \
+    else if (r.wave && r.k == 1) FP8SG_LN_FWD(IN, 1, true, false); \
+    else if (r.wave) FP8SG_LN_FWD(IN, 2, true, false);          \
+    else if (r.k == 1) FP8SG_LN_FWD(IN, 1, false, false);       \
+    else if (r.k == 2) FP8SG_LN_FWD(IN, 2, false, false);       \
+    else if (r.k == 3) FP8SG_LN_FWD(IN, 3, false, false);       \
+    else FP8SG_LN_FWD(IN, 8, false, false);                     \
   } while (0)
   if (p.x_type == kInBF16) FP8SG_LN_FWD_IN(kInBF16);
   else FP8SG_LN_FWD_IN(kInF32);
@@ -471,16 +486,17 @@ hipError_t launch_layernorm_bwd(const NormBwd& p, hipStream_t s) {
   const BwdShape b = bwd_shape(p.rows, p.cols, p.xhat != nullptr, p.x_type);
   if (b.grid > 0) {
     const unsigned lds = (unsigned)((b.groups - 1) * 8 * b.nt * sizeof(float));
-#define FP8SG_LN_BWD(IN, HELD, K)                                                        \
-  hipLaunchKernelGGL((k_ln_bwd<IN, HELD, K>), dim3(b.grid), dim3(b.nt * b.groups), lds, s, \
-                     p, b.nt, b.groups)
-#define FP8SG_LN_BWD_IN(IN, HELD)                \
-  do {                                           \
-    if (b.k == 1) FP8SG_LN_BWD(IN, HELD, 1);     \
-    else if (b.k == 2) FP8SG_LN_BWD(IN, HELD, 2); \
-    else if (b.k == 3) FP8SG_LN_BWD(IN, HELD, 3); \
-    else if (b.k == 4) FP8SG_LN_BWD(IN, HELD, 4); \
-    else FP8SG_LN_BWD(IN, HELD, 8);              \
+#define FP8SG_LN_BWD(IN, HELD, K, TINY)                                              \
+  hipLaunchKernelGGL((k_ln_bwd<IN, HELD, K, TINY>), dim3(b.grid), dim3(b.nt * b.groups), \
+                     lds, s, p, b.nt, b.groups)
+#define FP8SG_LN_BWD_IN(IN, HELD)                       \
+  do {                                                  \
+    if (p.cols < 8) FP8SG_LN_BWD(IN, HELD, 1, true);    \
+    else if (b.k == 1) FP8SG_LN_BWD(IN, HELD, 1, false); \
+    else if (b.k == 2) FP8SG_LN_BWD(IN, HELD, 2, false); \
+    else if (b.k == 3) FP8SG_LN_BWD(IN, HELD, 3, false); \
+    else if (b.k == 4) FP8SG_LN_BWD(IN, HELD, 4, false); \
+    else FP8SG_LN_BWD(IN, HELD, 8, false);              \
   } while (0)
     const int held = p.xhat ? p.xhat_fmt : kNotHeld;
     if (p.x_type == kInBF16) {

@@ -220,7 +220,7 @@ __device__ __forceinline__ void zero_padding(const MoeRows& p, int64_t block, ui
 
 // A wave takes K slots a lane of a token's row, all loaded before the first
 // is cast; blockIdx.y walks the row's shares.
-template <int K>
+template <int K, bool TINY>
 __global__ __launch_bounds__(kThreads) void k_moe_dispatch(const MoeRows p, int64_t token_blocks,
                                                            const uint16_t* __restrict__ x,
                                                            uint16_t* __restrict__ xs, CastOut xq) {
@@ -240,7 +240,9 @@ __global__ __launch_bounds__(kThreads) void k_moe_dispatch(const MoeRows p, int6
     SlotCast c[K];
 #pragma unroll
     for (int i = 0; i < K; ++i)
-      v[i].load(x + tok * p.cols, base + i * 512 + lane * 8, p.cols);
+      v[i].template load<TINY>(x + tok * p.cols, base + i * 512 + lane * 8, p.cols);
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i].template settle<TINY>(base + i * 512 + lane * 8, p.cols);
     if (xq.q) {
       float f[K][8];
 #pragma unroll
@@ -266,7 +268,7 @@ __global__ __launch_bounds__(kThreads) void k_moe_dispatch(const MoeRows p, int6
 
 // KJ choices at a time: their loads go out together, a dropped one's from
 // row 0 with its values put to zero (its row may hold anything).
-template <int KJ>
+template <int KJ, bool TINY>
 __global__ __launch_bounds__(kThreads) void k_moe_combine(const MoeRows p,
                                                           const uint16_t* __restrict__ ys,
                                                           const float* __restrict__ weight,
@@ -290,9 +292,10 @@ __global__ __launch_bounds__(kThreads) void k_moe_combine(const MoeRows p,
         const int64_t r = (uint32_t)p.pos[c];
         ok[j] = r < p.rows && j0 + j < p.k;
         wt[j] = weight ? weight[c] : 1.0f;
-        if (p.rows > 0) v[j].load(ys + (ok[j] ? r : 0) * p.cols, col, p.cols);
-        else v[j].zero();
+        v[j].template load<TINY>(ys + (ok[j] ? r : 0) * p.cols, col, p.cols);
       }
+#pragma unroll
+      for (int j = 0; j < KJ; ++j) v[j].template settle<TINY>(col, p.cols);
 #pragma unroll
       for (int j = 0; j < KJ; ++j)
 #pragma unroll
@@ -304,7 +307,7 @@ __global__ __launch_bounds__(kThreads) void k_moe_combine(const MoeRows p,
 
 // Gradient of combine.  A token's threads (a wave, or the workgroup) walk
 // its row once per KJ choices.
-template <int KJ, bool WAVE>
+template <int KJ, bool WAVE, bool TINY>
 __global__ __launch_bounds__(kThreads) void k_moe_combine_bwd(
     const MoeRows p, int64_t token_blocks, const uint16_t* __restrict__ dy,
     const uint16_t* __restrict__ ys, const float* __restrict__ weight,
@@ -315,6 +318,7 @@ __global__ __launch_bounds__(kThreads) void k_moe_combine_bwd(
   }
   __shared__ float red[KJ][kThreads / 64];
   constexpr int nt = WAVE ? 64 : kThreads;
+  constexpr int U = KJ <= 4 ? 2 : 1;           // slots a thread at a time
   const int t = threadIdx.x & (nt - 1);
   const int64_t tok = WAVE ? (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)
                            : (int64_t)blockIdx.x;
@@ -333,27 +337,34 @@ __global__ __launch_bounds__(kThreads) void k_moe_combine_bwd(
       wt[j] = weight[c];
       acc[j] = 0.0f;
     }
-    for (int slot = t; slot < slots; slot += nt) {
-      const int64_t col = (int64_t)slot * 8;
-      const int64_t left = p.cols - col;
-      const int nv = left < 8 ? (int)left : 8;
-      Slot<kInBF16> d, v[KJ];
-      d.load(dy + tok * p.cols, col, p.cols);
+    for (int first = t; first < slots; first += U * nt) {
+      Slot<kInBF16> d[U], v[U][KJ];
 #pragma unroll
-      for (int j = 0; j < KJ; ++j) {
-        if (p.rows > 0) v[j].load(ys + row[j] * p.cols, col, p.cols);
-        else v[j].zero();
+      for (int u = 0; u < U; ++u) {
+        const int64_t col = (int64_t)(first + u * nt) * 8;
+        d[u].template load<TINY>(dy + tok * p.cols, col, p.cols);
+#pragma unroll
+        for (int j = 0; j < KJ; ++j)
+          v[u][j].template load<TINY>(ys + row[j] * p.cols, col, p.cols);
       }
 #pragma unroll
-      for (int j = 0; j < KJ; ++j) {
-        if (!ok[j]) continue;
-        float o[8];
+      for (int u = 0; u < U; ++u) {
+        const int64_t col = (int64_t)(first + u * nt) * 8;
+        const int64_t left = p.cols - col;
+        const int nv = left < 8 ? (int)left : 8;
+        d[u].template settle<TINY>(col, p.cols);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          acc[j] += d.get(i) * v[j].get(i);
-          o[i] = wt[j] * d.get(i);
+        for (int j = 0; j < KJ; ++j) {
+          v[u][j].template settle<TINY>(col, p.cols);
+          if (!ok[j] || nv <= 0) continue;
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            acc[j] += d[u].get(i) * v[u][j].get(i);
+            o[i] = wt[j] * d[u].get(i);
+          }
+          store_bf16x8(dys + row[j] * p.cols + col, o, nv);
         }
-        store_bf16x8(dys + row[j] * p.cols + col, o, nv);
       }
     }
 #pragma unroll
@@ -423,12 +434,14 @@ hipError_t launch_moe_dispatch(const MoeRows& p, const uint16_t* x, uint16_t* xs
   const int k = shares == 1 || p.tokens * shares <= 4096 ? 1 : shares == 2 ? 2 : 4;
   const int64_t y = (shares + k - 1) / k;
   const dim3 grid((unsigned)gx, (unsigned)(y < 65535 ? y : 65535));
-  if (k == 1)
-    hipLaunchKernelGGL(k_moe_dispatch<1>, grid, dim3(kThreads), 0, s, p, tb, x, xs, xq);
+  if (p.cols < 8)
+    hipLaunchKernelGGL((k_moe_dispatch<1, true>), grid, dim3(kThreads), 0, s, p, tb, x, xs, xq);
+  else if (k == 1)
+    hipLaunchKernelGGL((k_moe_dispatch<1, false>), grid, dim3(kThreads), 0, s, p, tb, x, xs, xq);
   else if (k == 2)
-    hipLaunchKernelGGL(k_moe_dispatch<2>, grid, dim3(kThreads), 0, s, p, tb, x, xs, xq);
+    hipLaunchKernelGGL((k_moe_dispatch<2, false>), grid, dim3(kThreads), 0, s, p, tb, x, xs, xq);
   else
-    hipLaunchKernelGGL(k_moe_dispatch<4>, grid, dim3(kThreads), 0, s, p, tb, x, xs, xq);
+    hipLaunchKernelGGL((k_moe_dispatch<4, false>), grid, dim3(kThreads), 0, s, p, tb, x, xs, xq);
   return hipGetLastError();
 }
 
@@ -446,27 +459,39 @@ hipError_t launch_moe_dispatch(const MoeRows& p, const uint16_t* x, uint16_t* xs
     }                                                 \
   } while (0)
 
-hipError_t launch_moe_combine(const MoeRows& p, const uint16_t* ys, const float* weight,
+hipError_t launch_moe_combine(const MoeRows& rows, const uint16_t* ys, const float* weight,
                               uint16_t* y, hipStream_t s) {
+  MoeRows p = rows;
   if (p.tokens * p.cols == 0) return hipSuccess;
+  if (p.rows == 0) p.k = 0;                    // nothing to add up, or to read
   const int64_t g = tile_blocks(p.tokens, p.cols);
-  FP8SG_K_DISPATCH(p.k, hipLaunchKernelGGL(k_moe_combine<KJ>, dim3((unsigned)g), dim3(kThreads), 0,
-                                           s, p, ys, weight, y));
+  if (p.cols < 8)
+    hipLaunchKernelGGL((k_moe_combine<1, true>), dim3((unsigned)g), dim3(kThreads), 0, s, p, ys,
+                       weight, y);
+  else
+    FP8SG_K_DISPATCH(p.k, hipLaunchKernelGGL((k_moe_combine<KJ, false>), dim3((unsigned)g),
+                                             dim3(kThreads), 0, s, p, ys, weight, y));
   return hipGetLastError();
 }
 
 hipError_t launch_moe_combine_bwd(const MoeRows& p, const uint16_t* dy, const uint16_t* ys,
                                   const float* weight, uint16_t* dys, float* dw, hipStream_t s) {
+  if (p.rows == 0) ys = dy;                    // all choices dropped: read, not used
   const bool wave = p.tokens >= 2048 || p.cols <= 512;
   const int64_t tb = wave ? (p.tokens + kThreads / 64 - 1) / (kThreads / 64) : p.tokens;
   const int64_t g = tb + (p.cols > 0 ? pad_blocks(p.rows) : 0);
   if (g == 0) return hipSuccess;
+  if (p.cols < 8) {
+    hipLaunchKernelGGL((k_moe_combine_bwd<1, true, true>), dim3((unsigned)g), dim3(kThreads), 0, s,
+                       p, tb, dy, ys, weight, dys, dw);
+    return hipGetLastError();
+  }
   FP8SG_K_DISPATCH(p.k, {
     if (wave)
-      hipLaunchKernelGGL((k_moe_combine_bwd<KJ, true>), dim3((unsigned)g), dim3(kThreads), 0, s, p,
+      hipLaunchKernelGGL((k_moe_combine_bwd<KJ, true, false>), dim3((unsigned)g), dim3(kThreads), 0, s, p,
                          tb, dy, ys, weight, dys, dw);
     else
-      hipLaunchKernelGGL((k_moe_combine_bwd<KJ, false>), dim3((unsigned)g), dim3(kThreads), 0, s,
+      hipLaunchKernelGGL((k_moe_combine_bwd<KJ, false, false>), dim3((unsigned)g), dim3(kThreads), 0, s,
                          p, tb, dy, ys, weight, dys, dw);
   });
   return hipGetLastError();

@@ -81,19 +81,17 @@ struct Slot {
     }
     drop_words<kWords>(s >= 8);
   }
-  // Columns col .. col + 7 of a row of `cols`: one vector load on every path
-  // but that of rows of fewer than 8.  A wave with lanes at or past the
-  // row's end moves theirs back to its last 8 elements and drops the front.
-  // STREAM: read once, otherwise read again.
-  template <bool STREAM, class I>
+  // Columns col .. col + 7 of a row of `cols`.  One vector load without a
+  // branch: at or past the row's end, the row's last 8 elements, which
+  // settle() turns into the columns asked for, zeros past the end.  (The two
+  // are apart so that a load's wait comes where its values are used.)
+  // TINY: rows of fewer than 8 columns, element by element.
+  // load: read once; load_cached: read again.
+  template <bool TINY, bool STREAM, class I>
   __device__ __forceinline__ void load_any(const uint8_t* row, I col, I cols) {
     using U = std::make_unsigned_t<I>;
-    if (__all(cols - col >= 8)) {
-      load8<STREAM>(row + (U)col * kBytes);
-    } else if (cols >= 8) {
-      const I at = min(col, cols - 8);
-      load8<STREAM>(row + (U)at * kBytes);
-      drop((int)min(col - at, (I)8));
+    if constexpr (!TINY) {
+      load8<STREAM>(row + (U)min(col, cols - 8) * kBytes);
     } else {
       zero();
 #pragma unroll
@@ -108,17 +106,18 @@ struct Slot {
       }
     }
   }
-  template <class I>
-  __device__ __forceinline__ void load(const uint8_t* row, I col, I cols) {
-    load_any<true>(row, col, cols);
+  template <bool TINY, class T, class I>
+  __device__ __forceinline__ void load(const T* row, I col, I cols) {
+    load_any<TINY, true>(reinterpret_cast<const uint8_t*>(row), col, cols);
   }
-  template <class I>
-  __device__ __forceinline__ void load(const uint16_t* row, I col, I cols) {
-    load_any<true>(reinterpret_cast<const uint8_t*>(row), col, cols);
+  template <bool TINY, class T, class I>
+  __device__ __forceinline__ void load_cached(const T* row, I col, I cols) {
+    load_any<TINY, false>(reinterpret_cast<const uint8_t*>(row), col, cols);
   }
-  template <class I>
-  __device__ __forceinline__ void load_cached(const uint8_t* row, I col, I cols) {
-    load_any<false>(row, col, cols);
+  template <bool TINY, class I>
+  __device__ __forceinline__ void settle(I col, I cols) {
+    if constexpr (!TINY)
+      if (!__all(cols - col >= 8)) drop((int)min(max(col - (cols - 8), (I)0), (I)8));
   }
   __device__ __forceinline__ float get(int i) const {
     if constexpr (IN == kInBF16)
@@ -179,27 +178,29 @@ __device__ __forceinline__ void store_u8x8(uint8_t* p, uint2 b, int nv) {
       if (i < nv) p[i] = (uint8_t)((i < 4 ? b.x : b.y) >> (8 * (i & 3)));
   }
 }
-// Bytes col .. col + 7 of a row of `cols`, as Slot's load.
-template <class I>
+// Bytes col .. col + 7 of a row of `cols`, as Slot's load and settle.
+template <bool TINY, class I>
 __device__ __forceinline__ uint2 load_u8x8(const uint8_t* row, I col, I cols) {
   using U = std::make_unsigned_t<I>;
-  if (__all(cols - col >= 8)) {
-    const u32x2_a1 v =
-        __builtin_nontemporal_load(reinterpret_cast<const u32x2_a1*>(row + (U)col));
+  if constexpr (!TINY) {
+    const u32x2_a1 v = __builtin_nontemporal_load(
+        reinterpret_cast<const u32x2_a1*>(row + (U)min(col, cols - 8)));
     return make_uint2(v[0], v[1]);
-  }
-  uint64_t b = 0;
-  if (cols >= 8) {
-    const I at = min(col, cols - 8);
-    const u32x2_a1 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_a1*>(row + (U)at));
-    const I s = col - at;
-    b = s >= 8 ? 0 : (((uint64_t)v[1] << 32) | v[0]) >> (8 * (int)(s & 7));
   } else {
+    uint64_t b = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (col + i < cols) b |= (uint64_t)row[(U)col + i] << (8 * i);
+    return make_uint2((uint32_t)b, (uint32_t)(b >> 32));
   }
-  return make_uint2((uint32_t)b, (uint32_t)(b >> 32));
+}
+template <bool TINY, class I>
+__device__ __forceinline__ void settle_u8x8(uint2& v, I col, I cols) {
+  if constexpr (TINY) return;
+  if (__all(cols - col >= 8)) return;
+  const int s = (int)min(max(col - (cols - 8), (I)0), (I)8);
+  const uint64_t b = s >= 8 ? 0 : (((uint64_t)v.y << 32) | v.x) >> (8 * (s & 7));
+  v = make_uint2((uint32_t)b, (uint32_t)(b >> 32));
 }
 
 // Eight FP8 bytes' values.
