@@ -248,7 +248,7 @@ constexpr int bwd_threads(int k, bool held, int in) {
 template <int IN, int HELD, int K, bool TINY>
 __global__ __launch_bounds__(bwd_threads(K, HELD != kNotHeld, IN)) void k_ln_bwd(const NormBwd p, int nt,
                                                                int groups) {
-  constexpr bool AHEAD = K <= 4;
+  constexpr bool AHEAD = K <= 3 || (K == 4 && (HELD != kNotHeld || IN == kInBF16));
   __shared__ float red[2][2][16];
   extern __shared__ float sums[];            // [groups - 1][8][nt]
   // a wave is of one group

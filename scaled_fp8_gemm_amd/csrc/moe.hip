@@ -191,18 +191,21 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_sort(
   }
 }
 
-// Zeros for the padding rows inside segments, 16 rows per workgroup.
-constexpr int kPadRows = 16;
-__device__ __forceinline__ void zero_padding(const MoeRows& p, int64_t block, uint16_t* xs,
-                                             const CastOut& xq) {
+// Zeros for the padding rows inside segments, `share` (at most 16) rows per
+// workgroup: few in a small batch, where padding is most of the rows and
+// nothing else runs, 16 where most workgroups find none.
+int pad_share(int64_t rows) { return rows <= 1024 ? 1 : 16; }
+__device__ __forceinline__ void zero_padding(const MoeRows& p, int64_t block, int share,
+                                             uint16_t* xs, const CastOut& xq) {
   const int64_t end = min((int64_t)*p.end, p.rows);
   const float zero[8] = {};
   const int slots = (int)((p.cols + 7) >> 3);
-  const int64_t mine = block * kPadRows + (threadIdx.x & (kPadRows - 1));
+  const int at = threadIdx.x & 15;
+  const int64_t mine = block * share + at;
   // one load finds all of the workgroup's padding rows
-  uint32_t todo = (uint32_t)__ballot(mine < end && p.src[mine] < 0) & ((1u << kPadRows) - 1);
+  uint32_t todo = (uint32_t)__ballot(at < share && mine < end && p.src[mine] < 0) & 0xffffu;
   for (; todo; todo &= todo - 1) {
-    const int64_t r = block * kPadRows + __builtin_ctz(todo);
+    const int64_t r = block * share + __builtin_ctz(todo);
     for (int slot = threadIdx.x; slot < slots; slot += kThreads) {
       const int64_t left = p.cols - (int64_t)slot * 8;
       const int nv = left < 8 ? (int)left : 8;
@@ -222,10 +225,11 @@ __device__ __forceinline__ void zero_padding(const MoeRows& p, int64_t block, ui
 // is cast; blockIdx.y walks the row's shares.
 template <int K, bool TINY>
 __global__ __launch_bounds__(kThreads) void k_moe_dispatch(const MoeRows p, int64_t token_blocks,
+                                                           int share,
                                                            const uint16_t* __restrict__ x,
                                                            uint16_t* __restrict__ xs, CastOut xq) {
   if (blockIdx.x >= token_blocks) {
-    if (blockIdx.y == 0) zero_padding(p, blockIdx.x - token_blocks, xs, xq);
+    if (blockIdx.y == 0) zero_padding(p, blockIdx.x - token_blocks, share, xs, xq);
     return;
   }
   const float ts = xq.scaling == kCastTensor ? *xq.scale : 1.0f;
@@ -309,16 +313,15 @@ __global__ __launch_bounds__(kThreads) void k_moe_combine(const MoeRows p,
 // its row once per KJ choices.
 template <int KJ, bool WAVE, bool TINY>
 __global__ __launch_bounds__(kThreads) void k_moe_combine_bwd(
-    const MoeRows p, int64_t token_blocks, const uint16_t* __restrict__ dy,
+    const MoeRows p, int64_t token_blocks, int share, const uint16_t* __restrict__ dy,
     const uint16_t* __restrict__ ys, const float* __restrict__ weight,
     uint16_t* __restrict__ dys, float* __restrict__ dw) {
   if (blockIdx.x >= token_blocks) {
-    zero_padding(p, blockIdx.x - token_blocks, dys, CastOut());
+    zero_padding(p, blockIdx.x - token_blocks, share, dys, CastOut());
     return;
   }
   __shared__ float red[KJ][kThreads / 64];
   constexpr int nt = WAVE ? 64 : kThreads;
-  constexpr int U = KJ <= 4 ? 2 : 1;           // slots a thread at a time
   const int t = threadIdx.x & (nt - 1);
   const int64_t tok = WAVE ? (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)
                            : (int64_t)blockIdx.x;
@@ -337,34 +340,27 @@ __global__ __launch_bounds__(kThreads) void k_moe_combine_bwd(
       wt[j] = weight[c];
       acc[j] = 0.0f;
     }
-    for (int first = t; first < slots; first += U * nt) {
-      Slot<kInBF16> d[U], v[U][KJ];
+    for (int slot = t; slot < slots; slot += nt) {
+      const int64_t col = (int64_t)slot * 8;
+      const int64_t left = p.cols - col;
+      const int nv = left < 8 ? (int)left : 8;
+      Slot<kInBF16> d, v[KJ];
+      d.load<TINY>(dy + tok * p.cols, col, p.cols);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t col = (int64_t)(first + u * nt) * 8;
-        d[u].template load<TINY>(dy + tok * p.cols, col, p.cols);
+      for (int j = 0; j < KJ; ++j)
+        v[j].template load<TINY>(ys + row[j] * p.cols, col, p.cols);
+      d.settle<TINY>(col, p.cols);
 #pragma unroll
-        for (int j = 0; j < KJ; ++j)
-          v[u][j].template load<TINY>(ys + row[j] * p.cols, col, p.cols);
-      }
+      for (int j = 0; j < KJ; ++j) {
+        v[j].template settle<TINY>(col, p.cols);
+        if (!ok[j]) continue;
+        float o[8];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t col = (int64_t)(first + u * nt) * 8;
-        const int64_t left = p.cols - col;
-        const int nv = left < 8 ? (int)left : 8;
-        d[u].template settle<TINY>(col, p.cols);
-#pragma unroll
-        for (int j = 0; j < KJ; ++j) {
-          v[u][j].template settle<TINY>(col, p.cols);
-          if (!ok[j] || nv <= 0) continue;
-          float o[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            acc[j] += d[u].get(i) * v[u][j].get(i);
-            o[i] = wt[j] * d[u].get(i);
-          }
-          store_bf16x8(dys + row[j] * p.cols + col, o, nv);
+        for (int i = 0; i < 8; ++i) {
+          acc[j] += d.get(i) * v[j].get(i);
+          o[i] = wt[j] * d.get(i);
         }
+        store_bf16x8(dys + row[j] * p.cols + col, o, nv);
       }
     }
 #pragma unroll
@@ -398,7 +394,7 @@ int sort_blocks(int64_t n) {
   const int64_t c = sort_chunk(n);
   return n > 0 ? (int)((n + c - 1) / c) : 1;
 }
-int64_t pad_blocks(int64_t rows) { return (rows + kPadRows - 1) / kPadRows; }
+int64_t pad_blocks(int64_t rows) { return (rows + pad_share(rows) - 1) / pad_share(rows); }
 int64_t tile_blocks(int64_t rows, int64_t cols) {
   const int64_t need = (rows * ((cols + 127) / 128) + kGroups - 1) / kGroups;
   return need < ((int64_t)1 << 30) ? need : (int64_t)1 << 30;
@@ -428,6 +424,7 @@ hipError_t launch_moe_sort(const int32_t* expert, int64_t n, int experts, int pa
 hipError_t launch_moe_dispatch(const MoeRows& p, const uint16_t* x, uint16_t* xs,
                                const CastOut& xq, hipStream_t s) {
   if (p.rows == 0 || p.cols == 0) return hipSuccess;
+  const int share = pad_share(p.rows);
   const int64_t tb = (p.tokens + kWaves - 1) / kWaves, gx = tb + pad_blocks(p.rows);
   // as many waves as there are slots / 64 while the chip runs them at once
   const int64_t shares = (p.cols + 511) / 512;
@@ -435,13 +432,17 @@ hipError_t launch_moe_dispatch(const MoeRows& p, const uint16_t* x, uint16_t* xs
   const int64_t y = (shares + k - 1) / k;
   const dim3 grid((unsigned)gx, (unsigned)(y < 65535 ? y : 65535));
   if (p.cols < 8)
-    hipLaunchKernelGGL((k_moe_dispatch<1, true>), grid, dim3(kThreads), 0, s, p, tb, x, xs, xq);
+    hipLaunchKernelGGL((k_moe_dispatch<1, true>), grid, dim3(kThreads), 0, s, p, tb, share, x,
+                       xs, xq);
   else if (k == 1)
-    hipLaunchKernelGGL((k_moe_dispatch<1, false>), grid, dim3(kThreads), 0, s, p, tb, x, xs, xq);
+    hipLaunchKernelGGL((k_moe_dispatch<1, false>), grid, dim3(kThreads), 0, s, p, tb, share, x,
+                       xs, xq);
   else if (k == 2)
-    hipLaunchKernelGGL((k_moe_dispatch<2, false>), grid, dim3(kThreads), 0, s, p, tb, x, xs, xq);
+    hipLaunchKernelGGL((k_moe_dispatch<2, false>), grid, dim3(kThreads), 0, s, p, tb, share, x,
+                       xs, xq);
   else
-    hipLaunchKernelGGL((k_moe_dispatch<4, false>), grid, dim3(kThreads), 0, s, p, tb, x, xs, xq);
+    hipLaunchKernelGGL((k_moe_dispatch<4, false>), grid, dim3(kThreads), 0, s, p, tb, share, x,
+                       xs, xq);
   return hipGetLastError();
 }
 
@@ -476,6 +477,7 @@ hipError_t launch_moe_combine(const MoeRows& rows, const uint16_t* ys, const flo
 
 hipError_t launch_moe_combine_bwd(const MoeRows& p, const uint16_t* dy, const uint16_t* ys,
                                   const float* weight, uint16_t* dys, float* dw, hipStream_t s) {
+  const int share = pad_share(p.rows);
   if (p.rows == 0) ys = dy;                    // all choices dropped: read, not used
   const bool wave = p.tokens >= 2048 || p.cols <= 512;
   const int64_t tb = wave ? (p.tokens + kThreads / 64 - 1) / (kThreads / 64) : p.tokens;
@@ -483,16 +485,16 @@ hipError_t launch_moe_combine_bwd(const MoeRows& p, const uint16_t* dy, const ui
   if (g == 0) return hipSuccess;
   if (p.cols < 8) {
     hipLaunchKernelGGL((k_moe_combine_bwd<1, true, true>), dim3((unsigned)g), dim3(kThreads), 0, s,
-                       p, tb, dy, ys, weight, dys, dw);
+                       p, tb, share, dy, ys, weight, dys, dw);
     return hipGetLastError();
   }
   FP8SG_K_DISPATCH(p.k, {
     if (wave)
       hipLaunchKernelGGL((k_moe_combine_bwd<KJ, true, false>), dim3((unsigned)g), dim3(kThreads), 0, s, p,
-                         tb, dy, ys, weight, dys, dw);
+                         tb, share, dy, ys, weight, dys, dw);
     else
       hipLaunchKernelGGL((k_moe_combine_bwd<KJ, false, false>), dim3((unsigned)g), dim3(kThreads), 0, s,
-                         p, tb, dy, ys, weight, dys, dw);
+                         p, tb, share, dy, ys, weight, dys, dw);
   });
   return hipGetLastError();
 }

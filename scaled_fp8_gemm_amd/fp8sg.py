@@ -166,7 +166,8 @@ def _check(name: str, status: int):
 def _rc(x: torch.Tensor, name="x"):
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
-    return x.shape[0], x.shape[1]
+    rows, cols = x.shape
+    return rows, cols
 
 
 def workspace(device=None, wait_polls: int = 0, stream=None) -> torch.Tensor:
