@@ -132,7 +132,7 @@ __global__ __launch_bounds__(kThreads) void k_act_fwd(const ActFwd p) {
 #pragma unroll
       for (int i = 0; i < H; ++i) store_cast(p.ckpt, c[i], w.row * H + i, p.cols, slot, nv);
     }
-    if (p.y && nv > 0) store_bf16x8(p.y + w.row * p.cols + col, y, nv);
+    if (p.y && nv > 0) store_bf16x8(p.y + w.row * p.cols + col, y, nv, p.stream);
     if (p.yq.q) cast_store<false, 1>(p.yq, out, w.row, p.cols, slot, 0, ts);
     if (p.amax) amax = max(amax, absmax_f32x8(y));
   }
@@ -193,9 +193,9 @@ __global__ __launch_bounds__(kThreads) void k_act_bwd(const ActBwd p) {
       }
     }
     uint16_t* out = p.dh + hrow * p.cols + col;
-    store_bf16x8(out, da, nv);
-    if constexpr (GATED) store_bf16x8(out + p.cols, du, nv);
-    if (p.y) store_bf16x8(p.y + w.row * p.cols + col, y, nv);
+    store_bf16x8(out, da, nv, p.stream);
+    if constexpr (GATED) store_bf16x8(out + p.cols, du, nv, p.stream);
+    if (p.y) store_bf16x8(p.y + w.row * p.cols + col, y, nv, p.stream);
   }
 }
 
@@ -223,7 +223,7 @@ template <bool TINY>
 __global__ __launch_bounds__(kThreads) void k_ckpt_load(const uint8_t* __restrict__ q,
                                                         const float* __restrict__ scale_inv,
                                                         int fmt, int64_t rows, int64_t cols,
-                                                        uint16_t* __restrict__ y) {
+                                                        uint16_t* __restrict__ y, bool stream) {
   const int lane = threadIdx.x & 15;
   const int tiles = (int)((cols + 127) >> 7);
   TileWalk w((int64_t)blockIdx.x * kGroups + (threadIdx.x >> 4), (int64_t)gridDim.x * kGroups,
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(kThreads) void k_ckpt_load(const uint8_t* __restric
     const float s = scale_inv[w.row * tiles + w.tile];
     settle_u8x8<TINY>(b, col, cols);
     decode8(fmt, b, s, v);
-    store_bf16x8(y + at, v, nv);
+    store_bf16x8(y + at, v, nv, stream);
   }
 }
 
@@ -268,7 +268,12 @@ constexpr int64_t kAnyGrid = (int64_t)1 << 30;
 
 }  // namespace
 
-hipError_t launch_act_fwd(const ActFwd& p, hipStream_t s) {
+hipError_t launch_act_fwd(const ActFwd& act, hipStream_t s) {
+  ActFwd p = act;
+  const int halves = p.gated ? 2 : 1;
+  p.stream = p.yq.stream = p.ckpt.stream =
+      p.rows * p.cols * (halves * (p.ckpt.q ? 3 : 2) + (p.y ? 2 : 0) + (p.yq.q ? 1 : 0)) >
+      kStreamBytes;
   if (p.rows * p.cols == 0)
     return p.amax ? launch_amax_finalize(p.part, 0, p.amax, s) : hipSuccess;
   const int g = tile_grid(p.rows, p.cols, p.amax ? kMaxPartials : kAnyGrid);
@@ -283,7 +288,10 @@ hipError_t launch_act_fwd(const ActFwd& p, hipStream_t s) {
   return launch_amax_finalize(p.part, g, p.amax, s);
 }
 
-hipError_t launch_act_bwd(const ActBwd& p, hipStream_t s) {
+hipError_t launch_act_bwd(const ActBwd& act, hipStream_t s) {
+  ActBwd p = act;
+  const int halves = p.gated ? 2 : 1;
+  p.stream = p.rows * p.cols * (halves * (p.ckpt ? 3 : 4) + (p.y ? 4 : 2)) > kStreamBytes;
   if (p.rows * p.cols == 0) return hipSuccess;
   const int g = tile_grid(p.rows, p.cols, kAnyGrid);
   FP8SG_ACT_DISPATCH(p.act, p.gated, {
@@ -299,8 +307,10 @@ hipError_t launch_act_bwd(const ActBwd& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_checkpoint_save(const uint16_t* x, int64_t rows, int64_t cols, const CastOut& o,
-                                  hipStream_t s) {
+hipError_t launch_checkpoint_save(const uint16_t* x, int64_t rows, int64_t cols,
+                                  const CastOut& out, hipStream_t s) {
+  CastOut o = out;
+  o.stream = rows * cols * 3 > kStreamBytes;
   if (rows * cols == 0) return hipSuccess;
   if (cols % 128 == 0)
     return launch_quantize_block(x, rows, cols, o.fmt, 1, o.q, static_cast<float*>(o.scale_inv), s);
@@ -316,12 +326,13 @@ hipError_t launch_checkpoint_load(const uint8_t* q, const float* scale_inv, int 
                                   int64_t cols, uint16_t* y, hipStream_t s) {
   if (rows * cols == 0) return hipSuccess;
   const dim3 g(tile_grid(rows, cols, kAnyGrid));
+  const bool stream = rows * cols * 3 > kStreamBytes;
   if (cols < 8)
     hipLaunchKernelGGL(k_ckpt_load<true>, g, dim3(kThreads), 0, s, q, scale_inv, fmt, rows, cols,
-                       y);
+                       y, stream);
   else
     hipLaunchKernelGGL(k_ckpt_load<false>, g, dim3(kThreads), 0, s, q, scale_inv, fmt, rows, cols,
-                       y);
+                       y, stream);
   return hipGetLastError();
 }
 

@@ -157,7 +157,7 @@ __global__ __launch_bounds__(WAVE ? 256 : K == 2 ? 1024 : 512, fwd_waves(K, IN) 
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int slot = t + k * nt, nv = p.cols - slot * 8;
-        if (nv > 0) store_bf16x8(p.y + row * p.cols + (uint32_t)slot * 8, x[k], nv);
+        if (nv > 0) store_bf16x8(p.y + row * p.cols + (uint32_t)slot * 8, x[k], nv, p.stream);
       }
     }
     if (p.amax) {
@@ -347,7 +347,7 @@ __global__ __launch_bounds__(bwd_threads(K, HELD != kNotHeld, IN)) void k_ln_bwd
           for (int i = 0; i < 8; ++i) dx[i] = rstd * (dy[i] * gk[i]) - c1 - h[i] * c2h;
           const uint32_t at = (uint32_t)slot * 8;
           if constexpr (IN == kInBF16)
-            store_bf16x8(static_cast<uint16_t*>(p.dx) + row * p.cols + at, dx, nv);
+            store_bf16x8(static_cast<uint16_t*>(p.dx) + row * p.cols + at, dx, nv, false);
           else
             store_f32x8(static_cast<float*>(p.dx) + row * p.cols + at, dx, nv);
         }
@@ -451,7 +451,11 @@ BwdShape bwd_shape(int64_t rows, int64_t cols, bool held, int in) {
 
 }  // namespace
 
-hipError_t launch_layernorm_fwd(const NormFwd& p, hipStream_t s) {
+hipError_t launch_layernorm_fwd(const NormFwd& norm, hipStream_t s) {
+  NormFwd p = norm;
+  p.stream = p.yq.stream = p.xhat.stream =
+      p.rows * p.cols * ((p.x_type == kInBF16 ? 2 : 4) + (p.y ? 2 : 0) + (p.yq.q ? 1 : 0) +
+                         (p.xhat.q ? 1 : 0)) > kStreamBytes;
   if (p.rows == 0)
     return p.amax ? launch_amax_finalize(p.part, 0, p.amax, s) : hipSuccess;
   const RowShape r = row_shape(p.rows, p.cols);

@@ -209,7 +209,7 @@ __device__ __forceinline__ void zero_padding(const MoeRows& p, int64_t block, in
     for (int slot = threadIdx.x; slot < slots; slot += kThreads) {
       const int64_t left = p.cols - (int64_t)slot * 8;
       const int nv = left < 8 ? (int)left : 8;
-      if (xs) store_bf16x8(xs + r * p.cols + (int64_t)slot * 8, zero, nv);
+      if (xs) store_bf16x8(xs + r * p.cols + (int64_t)slot * 8, zero, nv, p.stream);
       if (xq.q) {
         SlotCast c;
         c.q = make_uint2(0, 0);
@@ -305,7 +305,7 @@ __global__ __launch_bounds__(kThreads) void k_moe_combine(const MoeRows p,
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] = ok[j] ? acc[i] + wt[j] * v[j].get(i) : acc[i];
     }
-    store_bf16x8(y + w.row * p.cols + col, acc, nv);
+    store_bf16x8(y + w.row * p.cols + col, acc, nv, p.stream);
   }
 }
 
@@ -360,7 +360,7 @@ __global__ __launch_bounds__(kThreads) void k_moe_combine_bwd(
           acc[j] += d.get(i) * v[j].get(i);
           o[i] = wt[j] * d.get(i);
         }
-        store_bf16x8(dys + row[j] * p.cols + col, o, nv);
+        store_bf16x8(dys + row[j] * p.cols + col, o, nv, p.stream);
       }
     }
 #pragma unroll
@@ -463,6 +463,7 @@ hipError_t launch_moe_dispatch(const MoeRows& p, const uint16_t* x, uint16_t* xs
 hipError_t launch_moe_combine(const MoeRows& rows, const uint16_t* ys, const float* weight,
                               uint16_t* y, hipStream_t s) {
   MoeRows p = rows;
+  p.stream = 2 * p.cols * (p.tokens + p.tokens * p.k) > kStreamBytes;
   if (p.tokens * p.cols == 0) return hipSuccess;
   if (p.rows == 0) p.k = 0;                    // nothing to add up, or to read
   const int64_t g = tile_blocks(p.tokens, p.cols);
@@ -475,8 +476,10 @@ hipError_t launch_moe_combine(const MoeRows& rows, const uint16_t* ys, const flo
   return hipGetLastError();
 }
 
-hipError_t launch_moe_combine_bwd(const MoeRows& p, const uint16_t* dy, const uint16_t* ys,
+hipError_t launch_moe_combine_bwd(const MoeRows& rows, const uint16_t* dy, const uint16_t* ys,
                                   const float* weight, uint16_t* dys, float* dw, hipStream_t s) {
+  MoeRows p = rows;
+  p.stream = 2 * p.cols * (p.tokens + 2 * p.rows) > kStreamBytes;
   const int share = pad_share(p.rows);
   if (p.rows == 0) ys = dy;                    // all choices dropped: read, not used
   const bool wave = p.tokens >= 2048 || p.cols <= 512;

@@ -127,12 +127,26 @@ struct Slot {
   }
 };
 
-__device__ __forceinline__ void store_bf16x8(uint16_t* p, const float (&y)[8], int nv) {
+// Keeps the two stores of a branch from being merged into one, which would
+// lose their difference.
+__device__ __forceinline__ void apart() { asm volatile(""); }
+// Stores.  stream (the same in all lanes): the call's tensors are too large
+// for a later reader to find them in a cache (kStreamBytes), so they are
+// written past it.
+__device__ __forceinline__ void store_bf16x8(uint16_t* p, const float (&y)[8], int nv,
+                                             bool stream) {
   if (nv >= 8) {
     u32x4_a2 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
-    *reinterpret_cast<u32x4_a2*>(p) = v;
+    u32x4_a2* q = reinterpret_cast<u32x4_a2*>(p);
+    if (stream) {
+      apart();
+      __builtin_nontemporal_store(v, q);
+      apart();
+    } else {
+      *q = v;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -167,11 +181,18 @@ __device__ __forceinline__ void store_f32x8(float* p, const float (&y)[8], int n
       if (i < nv) p[i] = y[i];
   }
 }
-__device__ __forceinline__ void store_u8x8(uint8_t* p, uint2 b, int nv) {
+__device__ __forceinline__ void store_u8x8(uint8_t* p, uint2 b, int nv, bool stream) {
   if (nv >= 8) {
     u32x2_a1 v;
     v[0] = b.x; v[1] = b.y;
-    *reinterpret_cast<u32x2_a1*>(p) = v;
+    u32x2_a1* q = reinterpret_cast<u32x2_a1*>(p);
+    if (stream) {
+      apart();
+      __builtin_nontemporal_store(v, q);
+      apart();
+    } else {
+      *q = v;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -389,7 +410,7 @@ __device__ __forceinline__ void cast_slots(int scaling, int fmt, const float (&y
 __device__ __forceinline__ void store_cast(const CastOut& o, const SlotCast& c, int64_t row,
                                            int64_t cols, int slot, int nv) {
   if (nv <= 0) return;
-  store_u8x8(o.q + row * cols + (int64_t)slot * 8, c.q, nv);
+  store_u8x8(o.q + row * cols + (int64_t)slot * 8, c.q, nv, o.stream);
   if (o.scaling == kCastBlock) {
     if ((slot & 15) == 0)
       static_cast<float*>(o.scale_inv)[row * ((cols + 127) >> 7) + (slot >> 4)] = c.scale_inv;
