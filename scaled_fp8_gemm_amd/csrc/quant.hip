@@ -16,7 +16,7 @@
 #include <atomic>
 #include <mutex>
 
-#include "fp8_device.h"
+#include "quant_common.h"
 #include "launch.h"
 
 namespace fp8sg {

@@ -13,7 +13,7 @@
 
 #include <type_traits>
 
-#include "fp8_device.h"
+#include "quant_common.h"
 #include "launch.h"
 
 namespace fp8sg {
