@@ -430,8 +430,8 @@ fp8_status_t fp8_layernorm_fwd(const void* x, int32_t x_type, const void* gamma,
                                void* y_bf16, float* mean, float* rstd, const fp8_cast_out_t* yq,
                                const fp8_cast_out_t* xhat, void* workspace, void* stream);
 
-/* Bytes of fp8_layernorm_bwd's workspace (one row of 2 cols floats for each
- * of its workgroups; 0 for rows = 0 or sizes that the call rejects). */
+/* Bytes of fp8_layernorm_bwd's workspace: a row of 2 cols floats for each of
+ * its workgroups, at most 256; 0 for rows = 0 or sizes that the call rejects. */
 int64_t fp8_layernorm_workspace_bytes(int64_t rows, int64_t cols);
 
 /* Layer norm's gradients, with g = dy gamma:

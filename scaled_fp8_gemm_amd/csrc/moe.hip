@@ -11,6 +11,11 @@
 // (dispatch's gradient is combine without weights.)  The sort is a counting
 // sort of the ids alone, a few microseconds; the rest is bound by HBM and
 // goes by token, so a token's row is read once however many experts take it.
+// Measured (one MI355X, us):
+//   sort of 16384 choices to 8 experts                  7.4  (16 tokens: 5.0)
+//   dispatch, 8192 tokens x 4096, k 2, blockwise cast  32    4.2 TB/s
+//   combine, 4096 tokens x 4096, k 6                   39.7  5.9 TB/s
+//   its gradient, 8192 tokens x 5120, k 2              84    5.0 TB/s
 #include "tile.h"
 
 namespace fp8sg {
@@ -222,7 +227,8 @@ __device__ __forceinline__ void zero_padding(const MoeRows& p, int64_t block, in
 }
 
 // A wave takes K slots a lane of a token's row, all loaded before the first
-// is cast; blockIdx.y walks the row's shares.
+// is cast; blockIdx.y walks the row's shares.  (By 16-lane groups of one slot
+// each: 42.3 us at 8192 tokens x 4096, against 32.)
 template <int K, bool TINY>
 __global__ __launch_bounds__(kThreads) void k_moe_dispatch(const MoeRows p, int64_t token_blocks,
                                                            int share,
