@@ -433,8 +433,9 @@ hipError_t launch_moe_dispatch(const MoeRows& p, const uint16_t* x, uint16_t* xs
   const int share = pad_share(p.rows);
   const int64_t tb = (p.tokens + kWaves - 1) / kWaves, gx = tb + pad_blocks(p.rows);
   // as many waves as there are slots / 64 while the chip runs them at once
+  // (4 slots a lane: 33.0 against 33.1 us at 8192 tokens x 4096)
   const int64_t shares = (p.cols + 511) / 512;
-  const int k = shares == 1 || p.tokens * shares <= 4096 ? 1 : shares == 2 ? 2 : 4;
+  const int k = shares == 1 || p.tokens * shares <= 4096 ? 1 : 2;
   const int64_t y = (shares + k - 1) / k;
   const dim3 grid((unsigned)gx, (unsigned)(y < 65535 ? y : 65535));
   if (p.cols < 8)
@@ -443,11 +444,8 @@ hipError_t launch_moe_dispatch(const MoeRows& p, const uint16_t* x, uint16_t* xs
   else if (k == 1)
     hipLaunchKernelGGL((k_moe_dispatch<1, false>), grid, dim3(kThreads), 0, s, p, tb, share, x,
                        xs, xq);
-  else if (k == 2)
-    hipLaunchKernelGGL((k_moe_dispatch<2, false>), grid, dim3(kThreads), 0, s, p, tb, share, x,
-                       xs, xq);
   else
-    hipLaunchKernelGGL((k_moe_dispatch<4, false>), grid, dim3(kThreads), 0, s, p, tb, share, x,
+    hipLaunchKernelGGL((k_moe_dispatch<2, false>), grid, dim3(kThreads), 0, s, p, tb, share, x,
                        xs, xq);
   return hipGetLastError();
 }

@@ -406,31 +406,36 @@ __device__ __forceinline__ void cast_slots(int scaling, int fmt, const float (&y
     for (int k = 0; k < K; ++k) c[k].q = narrow8<kE5M2>(v[k]);
   }
 }
-// Its place in row `row` of an output of `cols` columns.
+// Its place in row `row` of an output of `cols` columns.  I: int where the
+// row is the same in all lanes and its length an int, so that an address is a
+// scalar base and a 32-bit offset.
+template <class I>
 __device__ __forceinline__ void store_cast(const CastOut& o, const SlotCast& c, int64_t row,
-                                           int64_t cols, int slot, int nv) {
+                                           I cols, int slot, int nv) {
+  using U = std::make_unsigned_t<I>;
   if (nv <= 0) return;
-  store_u8x8(o.q + row * cols + (int64_t)slot * 8, c.q, nv, o.stream);
+  store_u8x8(o.q + row * cols + (U)slot * 8, c.q, nv, o.stream);
   if (o.scaling == kCastBlock) {
     if ((slot & 15) == 0)
-      static_cast<float*>(o.scale_inv)[row * ((cols + 127) >> 7) + (slot >> 4)] = c.scale_inv;
+      (static_cast<float*>(o.scale_inv) + row * ((cols + 127) >> 7))[(U)(slot >> 4)] =
+          c.scale_inv;
   } else if (o.scaling == kCastMX) {
     if ((slot & 3) == 0)
-      static_cast<uint8_t*>(o.scale_inv)[row * ((cols + 31) >> 5) + (slot >> 2)] =
+      (static_cast<uint8_t*>(o.scale_inv) + row * ((cols + 31) >> 5))[(U)(slot >> 2)] =
           (uint8_t)c.e8m0;
   }
 }
 // Slots first, first + step, ... of row `row`, cast and stored.  CHECKPOINT:
 // the output is known to have 1x128 tiles.
-template <bool CHECKPOINT, int K>
+template <bool CHECKPOINT, int K, class I>
 __device__ __forceinline__ void cast_store(const CastOut& o, const float (&y)[K][8], int64_t row,
-                                           int64_t cols, int first, int step, float ts) {
+                                           I cols, int first, int step, float ts) {
   SlotCast c[K];
   cast_slots<K>(CHECKPOINT ? (int)kCastBlock : o.scaling, o.fmt, y, ts, c);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int slot = first + k * step;
-    const int64_t left = cols - (int64_t)slot * 8;
+    const I left = cols - (I)slot * 8;
     store_cast(o, c[k], row, cols, slot, left < 8 ? (int)left : 8);
   }
 }
