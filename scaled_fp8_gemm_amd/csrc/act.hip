@@ -12,8 +12,8 @@
 // (each half of a gated row has tiles of its own).  All values between load
 // and store are FP32.  Bound by HBM: everything is read and written once.
 // Measured (one MI355X, us):
-//   gated SiLU forward 4096 x 11008, blockwise operand and checkpoint   58  5.5 TB/s
-//   GELU (tanh) backward 4096 x 49152 from the checkpoint, y again     230  6.2 TB/s
+//   gated SiLU forward 4096 x 11008, blockwise operand and checkpoint   59  5.4 TB/s
+//   GELU (tanh) backward 4096 x 49152 from the checkpoint, y again     229  6.2 TB/s
 //   checkpoint 8192 x 4096, save and load                               37  5.4 TB/s
 // against 5.1 TB/s of a large copy (one read for each write; these read less
 // or more).
@@ -254,7 +254,6 @@ int tile_grid(int64_t rows, int64_t cols, int64_t cap) {
   const int64_t need = (rows * ((cols + 127) / 128) + kGroups - 1) / kGroups;
   return (int)(need < cap ? need : cap);
 }
-constexpr int64_t kAnyGrid = (int64_t)1 << 30;
 
 #define FP8SG_ACT_DISPATCH(act, gated, ...)                          \
   do {                                                               \
@@ -282,7 +281,7 @@ hipError_t launch_act_fwd(const ActFwd& act, hipStream_t s) {
       kStreamBytes;
   if (p.rows * p.cols == 0)
     return p.amax ? launch_amax_finalize(p.part, 0, p.amax, s) : hipSuccess;
-  const int g = tile_grid(p.rows, p.cols, p.amax ? kMaxPartials : kAnyGrid);
+  const int g = tile_grid(p.rows, p.cols, p.amax ? kMaxPartials : kMaxGrid);
   FP8SG_ACT_DISPATCH(p.act, p.gated, {
     if (p.cols < 8)
       hipLaunchKernelGGL((k_act_fwd<A, G, true>), dim3(g), dim3(kThreads), 0, s, p);
@@ -299,7 +298,7 @@ hipError_t launch_act_bwd(const ActBwd& act, hipStream_t s) {
   const int halves = p.gated ? 2 : 1;
   p.stream = p.rows * p.cols * (halves * (p.ckpt ? 3 : 4) + (p.y ? 4 : 2)) > kStreamBytes;
   if (p.rows * p.cols == 0) return hipSuccess;
-  const int g = tile_grid(p.rows, p.cols, kAnyGrid);
+  const int g = tile_grid(p.rows, p.cols, kMaxGrid);
   FP8SG_ACT_DISPATCH(p.act, p.gated, {
     if (p.cols < 8 && p.ckpt)
       hipLaunchKernelGGL((k_act_bwd<A, G, true, true>), dim3(g), dim3(kThreads), 0, s, p);
@@ -320,7 +319,7 @@ hipError_t launch_checkpoint_save(const uint16_t* x, int64_t rows, int64_t cols,
   if (rows * cols == 0) return hipSuccess;
   if (cols % 128 == 0)
     return launch_quantize_block(x, rows, cols, o.fmt, 1, o.q, static_cast<float*>(o.scale_inv), s);
-  const dim3 g(tile_grid(rows, cols, kAnyGrid));
+  const dim3 g(tile_grid(rows, cols, kMaxGrid));
   if (cols < 8)
     hipLaunchKernelGGL(k_ckpt_save<true>, g, dim3(kThreads), 0, s, x, rows, cols, o);
   else
@@ -331,7 +330,7 @@ hipError_t launch_checkpoint_save(const uint16_t* x, int64_t rows, int64_t cols,
 hipError_t launch_checkpoint_load(const uint8_t* q, const float* scale_inv, int fmt, int64_t rows,
                                   int64_t cols, uint16_t* y, hipStream_t s) {
   if (rows * cols == 0) return hipSuccess;
-  const dim3 g(tile_grid(rows, cols, kAnyGrid));
+  const dim3 g(tile_grid(rows, cols, kMaxGrid));
   const bool stream = rows * cols * 3 > kStreamBytes;
   if (cols < 8)
     hipLaunchKernelGGL(k_ckpt_load<true>, g, dim3(kThreads), 0, s, q, scale_inv, fmt, rows, cols,

@@ -107,6 +107,9 @@ struct CastOut {
   int scaling = kCastNone;
   bool stream = false;    // written past the caches (set by the launchers)
 };
+// The most workgroups of a row operator's launch along x: a launch takes
+// fewer than 2^32 threads in all.  Kernels loop where this is not enough.
+constexpr int64_t kMaxGrid = (int64_t)1 << 22;
 // A row operator that reads and writes more than this, half of the last-level
 // cache, writes past the caches.  A chain of layer norm, GEMM, gated
 // activation and a reader of its output took 2 % less time so at 4096 x 22016

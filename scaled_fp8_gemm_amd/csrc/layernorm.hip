@@ -9,13 +9,13 @@
 // All sums are in FP32.  A row is read once and stays in registers between
 // its sums and its outputs (so the variance is taken about the mean, not from
 // a difference of two large sums).  Measured (one MI355X, us):
-//   forward 4096 x 12288 BF16, MX operand and checkpoint   51   4.0 TB/s
+//   forward 4096 x 12288 BF16, MX operand and checkpoint   49.5 4.1 TB/s
 //   forward 8192 x 4096, BF16 output alone                 26   5.1 TB/s
-//   backward 8192 x 5120 from the checkpoint               47.7 4.4 TB/s
+//   backward 8192 x 5120 from the checkpoint               47.6 4.4 TB/s
 //   backward 4096 x 12288 from x                           61   5.0 TB/s
 // against 5.1 TB/s of a large copy.  With two casts the forward pass is bound
-// by its instructions as much as by HBM (20.3 M wave instructions of VALU,
-// 33 us of the chip's issue slots); the backward pass by HBM and, at its end,
+// by its instructions as much as by HBM (19.0 M wave instructions of VALU,
+// 31 us of the chip's issue slots); the backward pass by HBM and, at its end,
 // by the second launch over the workgroups' partial sums (4.8 us).
 #include "tile.h"
 
@@ -256,8 +256,8 @@ constexpr int bwd_threads(int k, bool held, int in) {
   return k == 1 || (k == 2 && (held || in == kInBF16)) ? 1024 : 512;
 }
 template <int IN, int HELD, int K, bool TINY>
-__global__ __launch_bounds__(bwd_threads(K, HELD != kNotHeld, IN)) void k_ln_bwd(const NormBwd p, int nt,
-                                                               int groups) {
+__global__ __launch_bounds__(bwd_threads(K, HELD != kNotHeld, IN)) void k_ln_bwd(
+    const NormBwd p, int nt, int groups) {
   constexpr bool AHEAD = K <= 3 || (K == 4 && (HELD != kNotHeld || IN == kInBF16));
   __shared__ float red[2][2][16];
   extern __shared__ float sums[];            // [groups - 1][8][nt]
@@ -472,7 +472,8 @@ hipError_t launch_layernorm_fwd(const NormFwd& norm, hipStream_t s) {
   const int64_t need = r.wave ? (p.rows + kWaveRows - 1) / kWaveRows : p.rows;
   const int nt = r.wave ? 64 * kWaveRows : r.nt;
   // what a 256-CU device holds at once, rows dealt out evenly
-  const int64_t held = 256 * (fwd_waves(r.k, p.x_type) * 64 / nt), cap = held < kMaxPartials ? held : kMaxPartials;
+  const int64_t held = 256 * (fwd_waves(r.k, p.x_type) * 64 / nt);
+  const int64_t cap = held < kMaxPartials ? held : kMaxPartials;
   const int64_t rounds = (need + cap - 1) / cap;
   const int g = (int)((need + rounds - 1) / rounds);
 #define FP8SG_LN_FWD(IN, K, WAVE, TINY) \

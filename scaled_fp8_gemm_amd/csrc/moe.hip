@@ -13,9 +13,9 @@
 // goes by token, so a token's row is read once however many experts take it.
 // Measured (one MI355X, us):
 //   sort of 16384 choices to 8 experts                  7.4  (16 tokens: 5.0)
-//   dispatch, 8192 tokens x 4096, k 2, blockwise cast  32    4.2 TB/s
-//   combine, 4096 tokens x 4096, k 6                   39.7  5.9 TB/s
-//   its gradient, 8192 tokens x 5120, k 2              84    5.0 TB/s
+//   dispatch, 8192 tokens x 4096, k 2, blockwise cast  33    4.1 TB/s
+//   combine, 4096 tokens x 4096, k 6                   39.6  5.9 TB/s
+//   its gradient, 8192 tokens x 5120, k 2              82    5.1 TB/s
 #include "tile.h"
 
 namespace fp8sg {
@@ -200,27 +200,29 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_sort(
 // workgroup: few in a small batch, where padding is most of the rows and
 // nothing else runs, 16 where most workgroups find none.
 int pad_share(int64_t rows) { return rows <= 1024 ? 1 : 16; }
-__device__ __forceinline__ void zero_padding(const MoeRows& p, int64_t block, int share,
-                                             uint16_t* xs, const CastOut& xq) {
+__device__ __forceinline__ void zero_padding(const MoeRows& p, int64_t block, int64_t blocks,
+                                             int share, uint16_t* xs, const CastOut& xq) {
   const int64_t end = min((int64_t)*p.end, p.rows);
   const float zero[8] = {};
   const int slots = (int)((p.cols + 7) >> 3);
   const int at = threadIdx.x & 15;
-  const int64_t mine = block * share + at;
-  // one load finds all of the workgroup's padding rows
-  uint32_t todo = (uint32_t)__ballot(at < share && mine < end && p.src[mine] < 0) & 0xffffu;
-  for (; todo; todo &= todo - 1) {
-    const int64_t r = block * share + __builtin_ctz(todo);
-    for (int slot = threadIdx.x; slot < slots; slot += kThreads) {
-      const int64_t left = p.cols - (int64_t)slot * 8;
-      const int nv = left < 8 ? (int)left : 8;
-      if (xs) store_bf16x8(xs + r * p.cols + (int64_t)slot * 8, zero, nv, p.stream);
-      if (xq.q) {
-        SlotCast c;
-        c.q = make_uint2(0, 0);
-        if (xq.scaling == kCastMX) c.e8m0 = 127u;
-        else c.scale_inv = 1.0f;
-        store_cast(xq, c, r, p.cols, slot, nv);
+  for (int64_t first = block * share; first < end; first += blocks * share) {
+    // one load finds all of the padding rows among these
+    uint32_t todo = (uint32_t)__ballot(at < share && first + at < end && p.src[first + at] < 0) &
+                    0xffffu;
+    for (; todo; todo &= todo - 1) {
+      const int64_t r = first + __builtin_ctz(todo);
+      for (int slot = threadIdx.x; slot < slots; slot += kThreads) {
+        const int64_t left = p.cols - (int64_t)slot * 8;
+        const int nv = left < 8 ? (int)left : 8;
+        if (xs) store_bf16x8(xs + r * p.cols + (int64_t)slot * 8, zero, nv, p.stream);
+        if (xq.q) {
+          SlotCast c;
+          c.q = make_uint2(0, 0);
+          if (xq.scaling == kCastMX) c.e8m0 = 127u;
+          else c.scale_inv = 1.0f;
+          store_cast(xq, c, r, p.cols, slot, nv);
+        }
       }
     }
   }
@@ -228,49 +230,50 @@ __device__ __forceinline__ void zero_padding(const MoeRows& p, int64_t block, in
 
 // A wave takes K slots a lane of a token's row, all loaded before the first
 // is cast; blockIdx.y walks the row's shares.  (By 16-lane groups of one slot
-// each: 42.3 us at 8192 tokens x 4096, against 32.)
+// each: 42.3 us at 8192 tokens x 4096, against 33.)
 template <int K, bool TINY>
 __global__ __launch_bounds__(kThreads) void k_moe_dispatch(const MoeRows p, int64_t token_blocks,
                                                            int share,
                                                            const uint16_t* __restrict__ x,
                                                            uint16_t* __restrict__ xs, CastOut xq) {
   if (blockIdx.x >= token_blocks) {
-    if (blockIdx.y == 0) zero_padding(p, blockIdx.x - token_blocks, share, xs, xq);
+    if (blockIdx.y == 0)
+      zero_padding(p, blockIdx.x - token_blocks, gridDim.x - token_blocks, share, xs, xq);
     return;
   }
   const float ts = xq.scaling == kCastTensor ? *xq.scale : 1.0f;
   const int lane = threadIdx.x & 63;
-  const int64_t tok = (int64_t)blockIdx.x * kWaves +
-                      __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  if (tok >= p.tokens) return;
-  const int32_t* pos = p.pos + tok * p.k;
-  for (int64_t base = (int64_t)blockIdx.y * (K * 512); base < p.cols;
-       base += (int64_t)gridDim.y * (K * 512)) {
-    Slot<kInBF16> v[K];
-    SlotCast c[K];
-#pragma unroll
-    for (int i = 0; i < K; ++i)
-      v[i].template load<TINY>(x + tok * p.cols, base + i * 512 + lane * 8, p.cols);
-#pragma unroll
-    for (int i = 0; i < K; ++i) v[i].template settle<TINY>(base + i * 512 + lane * 8, p.cols);
-    if (xq.q) {
-      float f[K][8];
+  for (int64_t tok = (int64_t)blockIdx.x * kWaves +
+                     __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+       tok < p.tokens; tok += token_blocks * kWaves) {
+    for (int64_t base = (int64_t)blockIdx.y * (K * 512); base < p.cols;
+         base += (int64_t)gridDim.y * (K * 512)) {
+      Slot<kInBF16> v[K];
+      SlotCast c[K];
 #pragma unroll
       for (int i = 0; i < K; ++i)
+        v[i].template load<TINY>(x + tok * p.cols, base + i * 512 + lane * 8, p.cols);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[i][e] = v[i].get(e);
-      cast_slots<K>(xq.scaling, xq.fmt, f, ts, c);
-    }
-    for (int j = 0; j < p.k; ++j) {
-      const int64_t r = (uint32_t)pos[j];
-      if (r >= p.rows) continue;
+      for (int i = 0; i < K; ++i) v[i].template settle<TINY>(base + i * 512 + lane * 8, p.cols);
+      if (xq.q) {
+        float f[K][8];
 #pragma unroll
-      for (int i = 0; i < K; ++i) {
-        const int64_t col = base + i * 512 + lane * 8;
-        const int64_t left = p.cols - col;
-        const int nv = left < 8 ? (int)left : 8;
-        if (xs && nv > 0) store_slot(xs + r * p.cols + col, v[i], nv);
-        if (xq.q) store_cast(xq, c[i], r, p.cols, (int)(col >> 3), nv);
+        for (int i = 0; i < K; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[i][e] = v[i].get(e);
+        cast_slots<K>(xq.scaling, xq.fmt, f, ts, c);
+      }
+      for (int j = 0; j < p.k; ++j) {
+        const int64_t r = (uint32_t)p.pos[tok * p.k + j];
+        if (r >= p.rows) continue;
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+          const int64_t col = base + i * 512 + lane * 8;
+          const int64_t left = p.cols - col;
+          const int nv = left < 8 ? (int)left : 8;
+          if (xs && nv > 0) store_slot(xs + r * p.cols + col, v[i], nv);
+          if (xq.q) store_cast(xq, c[i], r, p.cols, (int)(col >> 3), nv);
+        }
       }
     }
   }
@@ -323,71 +326,72 @@ __global__ __launch_bounds__(kThreads) void k_moe_combine_bwd(
     const uint16_t* __restrict__ ys, const float* __restrict__ weight,
     uint16_t* __restrict__ dys, float* __restrict__ dw) {
   if (blockIdx.x >= token_blocks) {
-    zero_padding(p, blockIdx.x - token_blocks, share, dys, CastOut());
+    zero_padding(p, blockIdx.x - token_blocks, gridDim.x - token_blocks, share, dys, CastOut());
     return;
   }
   __shared__ float red[KJ][kThreads / 64];
   constexpr int nt = WAVE ? 64 : kThreads;
   const int t = threadIdx.x & (nt - 1);
-  const int64_t tok = WAVE ? (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)
-                           : (int64_t)blockIdx.x;
-  if (tok >= p.tokens) return;
   const int slots = (int)((p.cols + 7) >> 3);
-  for (int j0 = 0; j0 < p.k; j0 += KJ) {
-    float acc[KJ], wt[KJ];
-    int64_t row[KJ];
-    bool ok[KJ];
-#pragma unroll
-    for (int j = 0; j < KJ; ++j) {
-      const int64_t c = tok * p.k + min(j0 + j, p.k - 1);
-      const int64_t r = (uint32_t)p.pos[c];
-      ok[j] = r < p.rows && j0 + j < p.k;
-      row[j] = ok[j] ? r : 0;
-      wt[j] = weight[c];
-      acc[j] = 0.0f;
-    }
-    for (int slot = t; slot < slots; slot += nt) {
-      const int64_t col = (int64_t)slot * 8;
-      const int64_t left = p.cols - col;
-      const int nv = left < 8 ? (int)left : 8;
-      Slot<kInBF16> d, v[KJ];
-      d.load<TINY>(dy + tok * p.cols, col, p.cols);
-#pragma unroll
-      for (int j = 0; j < KJ; ++j)
-        v[j].template load<TINY>(ys + row[j] * p.cols, col, p.cols);
-      d.settle<TINY>(col, p.cols);
+  for (int64_t tok = WAVE ? (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6)
+                          : (int64_t)blockIdx.x;
+       tok < p.tokens; tok += token_blocks * (WAVE ? kWaves : 1)) {
+    for (int j0 = 0; j0 < p.k; j0 += KJ) {
+      float acc[KJ], wt[KJ];
+      int64_t row[KJ];
+      bool ok[KJ];
 #pragma unroll
       for (int j = 0; j < KJ; ++j) {
-        v[j].template settle<TINY>(col, p.cols);
-        if (!ok[j]) continue;
-        float o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          acc[j] += d.get(i) * v[j].get(i);
-          o[i] = wt[j] * d.get(i);
-        }
-        store_bf16x8(dys + row[j] * p.cols + col, o, nv, p.stream);
+        const int64_t c = tok * p.k + min(j0 + j, p.k - 1);
+        const int64_t r = (uint32_t)p.pos[c];
+        ok[j] = r < p.rows && j0 + j < p.k;
+        row[j] = ok[j] ? r : 0;
+        wt[j] = weight[c];
+        acc[j] = 0.0f;
       }
-    }
+      for (int slot = t; slot < slots; slot += nt) {
+        const int64_t col = (int64_t)slot * 8;
+        const int64_t left = p.cols - col;
+        const int nv = left < 8 ? (int)left : 8;
+        Slot<kInBF16> d, v[KJ];
+        d.load<TINY>(dy + tok * p.cols, col, p.cols);
 #pragma unroll
-    for (int j = 0; j < KJ; ++j) {
-      acc[j] = wave_sum(acc[j]);
-      if (!WAVE && (threadIdx.x & 63) == 0) red[j][threadIdx.x >> 6] = acc[j];
-    }
-    if constexpr (!WAVE) __syncthreads();
-    if (t < KJ && j0 + t < p.k) {
-      float s = 0.0f;
-      bool live = false;
+        for (int j = 0; j < KJ; ++j)
+          v[j].template load<TINY>(ys + row[j] * p.cols, col, p.cols);
+        d.settle<TINY>(col, p.cols);
 #pragma unroll
-      for (int j = 0; j < KJ; ++j)
-        if (j == t) {
-          live = ok[j];
-          s = acc[j];
+        for (int j = 0; j < KJ; ++j) {
+          v[j].template settle<TINY>(col, p.cols);
+          if (!ok[j]) continue;
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            acc[j] += d.get(i) * v[j].get(i);
+            o[i] = wt[j] * d.get(i);
+          }
+          store_bf16x8(dys + row[j] * p.cols + col, o, nv, p.stream);
         }
-      if constexpr (!WAVE) s = red[t][0] + red[t][1] + red[t][2] + red[t][3];
-      dw[tok * p.k + j0 + t] = live ? s : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < KJ; ++j) {
+        acc[j] = wave_sum(acc[j]);
+        if (!WAVE && (threadIdx.x & 63) == 0) red[j][threadIdx.x >> 6] = acc[j];
+      }
+      if constexpr (!WAVE) __syncthreads();
+      if (t < KJ && j0 + t < p.k) {
+        float s = 0.0f;
+        bool live = false;
+#pragma unroll
+        for (int j = 0; j < KJ; ++j)
+          if (j == t) {
+            live = ok[j];
+            s = acc[j];
+          }
+        if constexpr (!WAVE) s = red[t][0] + red[t][1] + red[t][2] + red[t][3];
+        dw[tok * p.k + j0 + t] = live ? s : 0.0f;
+      }
+      if constexpr (!WAVE) __syncthreads();
     }
-    if constexpr (!WAVE) __syncthreads();
   }
 }
 
@@ -400,10 +404,13 @@ int sort_blocks(int64_t n) {
   const int64_t c = sort_chunk(n);
   return n > 0 ? (int)((n + c - 1) / c) : 1;
 }
-int64_t pad_blocks(int64_t rows) { return (rows + pad_share(rows) - 1) / pad_share(rows); }
+int64_t at_most(int64_t n) { return n < kMaxGrid ? n : kMaxGrid; }
+int64_t pad_blocks(int64_t rows) {
+  return at_most((rows + pad_share(rows) - 1) / pad_share(rows));
+}
 int64_t tile_blocks(int64_t rows, int64_t cols) {
   const int64_t need = (rows * ((cols + 127) / 128) + kGroups - 1) / kGroups;
-  return need < ((int64_t)1 << 30) ? need : (int64_t)1 << 30;
+  return at_most(need);
 }
 
 }  // namespace
@@ -431,7 +438,7 @@ hipError_t launch_moe_dispatch(const MoeRows& p, const uint16_t* x, uint16_t* xs
                                const CastOut& xq, hipStream_t s) {
   if (p.rows == 0 || p.cols == 0) return hipSuccess;
   const int share = pad_share(p.rows);
-  const int64_t tb = (p.tokens + kWaves - 1) / kWaves, gx = tb + pad_blocks(p.rows);
+  const int64_t tb = at_most((p.tokens + kWaves - 1) / kWaves), gx = tb + pad_blocks(p.rows);
   // as many waves as there are slots / 64 while the chip runs them at once
   // (4 slots a lane: 33.0 against 33.1 us at 8192 tokens x 4096)
   const int64_t shares = (p.cols + 511) / 512;
@@ -487,7 +494,7 @@ hipError_t launch_moe_combine_bwd(const MoeRows& rows, const uint16_t* dy, const
   const int share = pad_share(p.rows);
   if (p.rows == 0) ys = dy;                    // all choices dropped: read, not used
   const bool wave = p.tokens >= 2048 || p.cols <= 512;
-  const int64_t tb = wave ? (p.tokens + kThreads / 64 - 1) / (kThreads / 64) : p.tokens;
+  const int64_t tb = at_most(wave ? (p.tokens + kWaves - 1) / kWaves : p.tokens);
   const int64_t g = tb + (p.cols > 0 ? pad_blocks(p.rows) : 0);
   if (g == 0) return hipSuccess;
   if (p.cols < 8) {
@@ -497,11 +504,11 @@ hipError_t launch_moe_combine_bwd(const MoeRows& rows, const uint16_t* dy, const
   }
   FP8SG_K_DISPATCH(p.k, {
     if (wave)
-      hipLaunchKernelGGL((k_moe_combine_bwd<KJ, true, false>), dim3((unsigned)g), dim3(kThreads), 0, s, p,
-                         tb, share, dy, ys, weight, dys, dw);
+      hipLaunchKernelGGL((k_moe_combine_bwd<KJ, true, false>), dim3((unsigned)g), dim3(kThreads), 0,
+                         s, p, tb, share, dy, ys, weight, dys, dw);
     else
-      hipLaunchKernelGGL((k_moe_combine_bwd<KJ, false, false>), dim3((unsigned)g), dim3(kThreads), 0, s,
-                         p, tb, share, dy, ys, weight, dys, dw);
+      hipLaunchKernelGGL((k_moe_combine_bwd<KJ, false, false>), dim3((unsigned)g), dim3(kThreads), 0,
+                         s, p, tb, share, dy, ys, weight, dys, dw);
   });
   return hipGetLastError();
 }

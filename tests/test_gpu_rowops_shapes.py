@@ -181,3 +181,36 @@ def test_dispatch_shares(F, tokens, k, experts, cols, pad):  # noqa: F811
     q2, s2, c2 = make_cast(F, end, cols, BLOCK)
     F.fp8_checkpoint_save(xs[:end].contiguous(), c2)
     assert torch.equal(q[:end], q2) and torch.equal(s[:end], s2)
+
+
+def test_more_rows_than_one_grid(F):  # noqa: F811
+    """Rows beyond what one launch's threads reach: the kernels loop."""
+    tokens, cols = (1 << 24) + 21, 8
+    x = torch.arange(tokens * cols, dtype=torch.int32, device=DEV).view(tokens, cols)
+    x = (x % 251 - 125).to(torch.bfloat16)
+    pos = torch.arange(tokens - 1, -1, -1, dtype=torch.int32, device=DEV).view(tokens, 1)
+    off = torch.tensor([0, tokens], dtype=torch.int32, device=DEV)
+    xs, y, dys = (empty(torch.bfloat16, tokens, cols) for _ in range(3))
+    F.fp8_moe_dispatch(x, pos, pos.view(-1), off, xs)
+    assert torch.equal(xs, x.flip(0))
+    F.fp8_moe_combine(xs, pos, None, y)
+    assert torch.equal(y, x)
+    w, dw = torch.full((tokens, 1), 2.0, device=DEV), empty(torch.float32, tokens, 1)
+    F.fp8_moe_combine_bwd(x, xs, w, pos, pos.view(-1), off, dys, dw)
+    assert torch.equal(dys, 2 * xs)
+    assert torch.equal(dw[:, 0], (x.float() ** 2).sum(1))     # whole numbers below 2^24
+    # padding rows: none of 2^26 + 37 rows is a token's
+    rows = (1 << 26) + 37
+    src = torch.full((rows,), -1, dtype=torch.int32, device=DEV)
+    off = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    none = torch.full((1, 1), -1, dtype=torch.int32, device=DEV)
+    xs = torch.ones((rows, 1), dtype=torch.bfloat16, device=DEV)
+    F.fp8_moe_dispatch(torch.ones_like(xs[:1]), none, src, off, xs)
+    assert not xs.any()
+    # one tile a row
+    v = torch.arange(rows, dtype=torch.int32, device=DEV).view(rows, 1)
+    v = (v % 97 - 48).to(torch.bfloat16)
+    q, s, ck = make_cast(F, rows, 1, BLOCK)
+    F.fp8_checkpoint_save(v, ck)
+    F.fp8_checkpoint_load(F.operand(q, F.E4M3, F.SCALE_BLOCK_1x128, s), rows, 1, xs)
+    assert torch.equal(xs, v)                                 # +-448 / (448 / |v|)
