@@ -17,6 +17,7 @@
 // by its instructions as much as by HBM (19.0 M wave instructions of VALU,
 // 31 us of the chip's issue slots); the backward pass by HBM and, at its end,
 // by the second launch over the workgroups' partial sums (4.8 us).
+#include "norm_shape.h"
 #include "tile.h"
 
 namespace fp8sg {
@@ -74,12 +75,8 @@ __device__ __forceinline__ void load_weight8(const void* w, int type, int col, i
 // rows with gamma and beta in registers, and the next row's loads go out
 // before the present row's sums.  K = 8 (rows above 16384 columns) has
 // registers for neither.
-// Waves of a CU by registers:
-constexpr int fwd_waves(int k, int in) {
-  return k == 1 ? 32 : k == 2 || (k == 3 && in == kInBF16) ? 16 : 8;
-}
 template <int IN, int K, bool WAVE, bool TINY>
-__global__ __launch_bounds__(WAVE ? 256 : K == 2 ? 1024 : 512, fwd_waves(K, IN) / 4) void k_ln_fwd(
+__global__ __launch_bounds__(WAVE ? 256 : K == 2 ? 1024 : 512, fwd_waves(K, IN == kInF32) / 4) void k_ln_fwd(
     const NormFwd p) {
   constexpr bool AHEAD = K <= 3;
   __shared__ float red[2][16];
@@ -251,12 +248,8 @@ struct BwdSlot {
   }
 };
 
-// Threads of a workgroup: 1024 while 128 registers are enough.
-constexpr int bwd_threads(int k, bool held, int in) {
-  return k == 1 || (k == 2 && (held || in == kInBF16)) ? 1024 : 512;
-}
 template <int IN, int HELD, int K, bool TINY>
-__global__ __launch_bounds__(bwd_threads(K, HELD != kNotHeld, IN)) void k_ln_bwd(
+__global__ __launch_bounds__(bwd_threads(K, HELD != kNotHeld, IN == kInF32)) void k_ln_bwd(
     const NormBwd p, int nt, int groups) {
   constexpr bool AHEAD = K <= 3 || (K == 4 && (HELD != kNotHeld || IN == kInBF16));
   __shared__ float red[2][2][16];
@@ -421,44 +414,6 @@ __global__ __launch_bounds__(1024) void k_ln_bwd_sum(const float* __restrict__ p
   }
 }
 
-// How a row of `cols` columns is dealt out: K slots to each of nt threads.
-struct RowShape {
-  int k, nt;
-  bool wave;
-};
-int round_up64(int n) { return (n + 63) / 64 * 64; }
-RowShape row_shape(int64_t rows, int64_t cols) {
-  const int slots = (int)((cols + 7) / 8);
-  // few rows: one slot a thread, for the shortest way through the row
-  if (rows <= 256 && slots > 64 && slots <= 512) return {1, round_up64(slots), false};
-  if (slots <= 64) return {1, 64, true};
-  if (slots <= 128) return {2, 64, true};
-  // 4, 8 or 16 waves, which spread evenly over a CU's SIMDs
-  if (slots <= 768) return {(slots + 255) / 256, 256, false};
-  if (slots <= 1536) return {(slots + 511) / 512, 512, false};
-  if (slots <= 2048) return {2, 1024, false};
-  return {8, 512, false};
-}
-// The backward pass: `groups` rows of a workgroup at a time, as many as its
-// threads allow, fewer where all 256 CUs would not get a workgroup.
-struct BwdShape {
-  int k, nt, groups, grid;
-};
-BwdShape bwd_shape(int64_t rows, int64_t cols, bool held, int in) {
-  const int slots = (int)((cols + 7) / 8);
-  BwdShape b;
-  const int64_t even = (rows + 255) / 256;
-  // one slot a thread where all rows are in registers at once even so
-  b.k = slots <= 64 || even * round_up64(slots) <= 1024 ? 1 : slots <= 1024 ? 2
-        : slots <= 1536 ? 3 : slots <= 2048 ? 4 : 8;
-  b.nt = b.k > 2 ? 512 : round_up64((slots + b.k - 1) / b.k);
-  const int64_t most = bwd_threads(b.k, held, in) / b.nt;
-  b.groups = (int)(even < most ? (even > 1 ? even : 1) : most);
-  const int64_t need = (rows + b.groups - 1) / b.groups;
-  b.grid = (int)(need < 256 ? need : 256);
-  return b;
-}
-
 }  // namespace
 
 hipError_t launch_layernorm_fwd(const NormFwd& norm, hipStream_t s) {
@@ -472,7 +427,7 @@ hipError_t launch_layernorm_fwd(const NormFwd& norm, hipStream_t s) {
   const int64_t need = r.wave ? (p.rows + kWaveRows - 1) / kWaveRows : p.rows;
   const int nt = r.wave ? 64 * kWaveRows : r.nt;
   // what a 256-CU device holds at once, rows dealt out evenly
-  const int64_t held = 256 * (fwd_waves(r.k, p.x_type) * 64 / nt);
+  const int64_t held = 256 * (fwd_waves(r.k, p.x_type == kInF32) * 64 / nt);
   const int64_t cap = held < kMaxPartials ? held : kMaxPartials;
   const int64_t rounds = (need + cap - 1) / cap;
   const int g = (int)((need + rounds - 1) / rounds);
@@ -498,7 +453,7 @@ hipError_t launch_layernorm_fwd(const NormFwd& norm, hipStream_t s) {
 int layernorm_bwd_partials(int64_t rows) { return (int)(rows < 256 ? rows : 256); }
 
 hipError_t launch_layernorm_bwd(const NormBwd& p, hipStream_t s) {
-  const BwdShape b = bwd_shape(p.rows, p.cols, p.xhat != nullptr, p.x_type);
+  const BwdShape b = bwd_shape(p.rows, p.cols, p.xhat != nullptr, p.x_type == kInF32);
   if (b.grid > 0) {
     const unsigned lds = (unsigned)((b.groups - 1) * 8 * b.nt * sizeof(float));
 #define FP8SG_LN_BWD(IN, HELD, K, TINY)                                              \
