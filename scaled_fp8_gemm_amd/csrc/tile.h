@@ -440,15 +440,20 @@ __device__ __forceinline__ void cast_store(const CastOut& o, const float (&y)[K]
   }
 }
 
-// Sum over the wave; every lane gets the result, the same bits.
+// Sum over the wave; every lane gets the result, the same bits: each step
+// pairs two sums and gives both of their lanes the same addition.  (Lanes of a
+// quad hold one value, so a mirrored half row is a partner's quad and a
+// mirrored row its half; rotations would give the quads of a row their four
+// sums in different orders.)
+constexpr int kDppMirror8 = 0x141, kDppMirror16 = 0x140;
 __device__ __forceinline__ float wave_sum(float v) {
   const auto move = [](auto ctrl, float x) {
     return __uint_as_float(dpp<decltype(ctrl)::value>(__float_as_uint(x)));
   };
   v += move(std::integral_constant<int, kDppXor1>{}, v);
   v += move(std::integral_constant<int, kDppXor2>{}, v);
-  v += move(std::integral_constant<int, kDppRor4>{}, v);
-  v += move(std::integral_constant<int, kDppRor8>{}, v);
+  v += move(std::integral_constant<int, kDppMirror8>{}, v);
+  v += move(std::integral_constant<int, kDppMirror16>{}, v);
   const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false,
                                                   false);
   v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
