@@ -8,7 +8,10 @@
 //
 // All sums are in FP32.  A row is read once and stays in registers between
 // its sums and its outputs (so the variance is taken about the mean, not from
-// a difference of two large sums).  Measured (one MI355X, us):
+// a difference of two large sums).  FP32 rows correct their mean by that of
+// the deviations, which comes with the squares' sum (8192 x 4096, BF16 output:
+// 39.2 us without, 40.0 so, 40.6 with a sum of its own; 4096 x 12288: 56.2,
+// 58.7, 61.0).  Measured (one MI355X, us):
 //   forward 4096 x 12288 BF16, MX operand and checkpoint   49.5 4.1 TB/s
 //   forward 8192 x 4096, BF16 output alone                 26   5.1 TB/s
 //   backward 8192 x 5120 from the checkpoint               47.6 4.4 TB/s
@@ -37,6 +40,25 @@ __device__ __forceinline__ float row_sum(float v, float* red, int nw) {
   __syncthreads();
   float s = 0.0f;
   for (int i = 0; i < nw; ++i) s += red[i];
+  return s;
+}
+
+// Two sums behind one barrier.
+template <bool WAVE>
+__device__ __forceinline__ float2 row_sum2(float a, float b, float* reda, float* redb, int nw) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  if constexpr (WAVE) return make_float2(a, b);
+  if ((threadIdx.x & 63) == 0) {
+    reda[threadIdx.x >> 6] = a;
+    redb[threadIdx.x >> 6] = b;
+  }
+  __syncthreads();
+  float2 s = make_float2(0.0f, 0.0f);
+  for (int i = 0; i < nw; ++i) {
+    s.x += reda[i];
+    s.y += redb[i];
+  }
   return s;
 }
 
@@ -79,7 +101,8 @@ template <int IN, int K, bool WAVE, bool TINY>
 __global__ __launch_bounds__(WAVE ? 256 : K == 2 ? 1024 : 512, fwd_waves(K, IN == kInF32) / 4) void k_ln_fwd(
     const NormFwd p) {
   constexpr bool AHEAD = K <= 3;
-  __shared__ float red[2][16];
+  constexpr int SUMS = IN == kInF32 ? 4 : 2;   // of a row
+  __shared__ float red[SUMS][16];
   __shared__ uint32_t redm[16];
   const int nt = WAVE ? 64 : blockDim.x;
   const int thread = WAVE ? threadIdx.x & 63 : threadIdx.x;
@@ -122,23 +145,68 @@ __global__ __launch_bounds__(WAVE ? 256 : K == 2 ? 1024 : 512, fwd_waves(K, IN =
       sum += s;
     }
     if constexpr (AHEAD) fetch(row + step);
-    const float mean = row_sum<WAVE>(sum, red[0], nw) / n;   // exact for a row of one value
-    float sq = 0.0f;
+    float mean = row_sum<WAVE>(sum, red[0], nw) / n;
+    const auto square = [&](float by) {          // sum of (x - by)^2, x left so
+      float sq = 0.0f;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int nv = p.cols - (t + k * nt) * 8;
+      for (int k = 0; k < K; ++k) {
+        const int nv = p.cols - (t + k * nt) * 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[k][i] -= mean;
-      if (!__all(nv >= 8)) {
+        for (int i = 0; i < 8; ++i) x[k][i] -= by;
+        if (!__all(nv >= 8)) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[k][i] = i < nv ? x[k][i] : 0.0f;
+          for (int i = 0; i < 8; ++i) x[k][i] = i < nv ? x[k][i] : 0.0f;
+        }
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += x[k][i] * x[k][i];
+        sq += s;
       }
-      float s = 0.0f;
+      return sq;
+    };
+    float var;
+    if constexpr (IN == kInBF16) {
+      var = row_sum<WAVE>(square(mean), red[1], nw) / n;
+    } else {
+      // The sum of 24-bit values is rounded, by more than the row's spread
+      // where the mean is large against it, so the mean is corrected by that
+      // of the deviations, which are small there: a row of one value ends at
+      // that value.  (BF16 needs none: sums of up to 2^16 values of 8 bits
+      // that share an exponent are exact in 24.)
+      const float sq = square(mean);
+      float off = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += x[k][i] * x[k][i];
-      sq += s;
+      for (int k = 0; k < K; ++k) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += x[k][i];
+        off += s;
+      }
+      float2 both = row_sum2<WAVE>(sq, off, red[1], red[2], nw);
+      both.x /= n;
+      both.y /= n;
+      // a row that holds an infinity keeps its mean
+      const float to = __builtin_isfinite(both.y) ? mean + both.y : mean;
+      const float by = to - mean;
+      mean = to;
+      // about the corrected mean: (d - by)^2 on average; afresh where the
+      // difference would lose bits (the same for the whole row)
+      var = both.x - by * (2.0f * both.y - by);
+      if (both.y * both.y > 0.25f * both.x) {
+        var = row_sum<WAVE>(square(by), red[3], nw) / n;
+      } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const int nv = p.cols - (t + k * nt) * 8;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[k][i] -= by;
+          if (!__all(nv >= 8)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[k][i] = i < nv ? x[k][i] : 0.0f;
+          }
+        }
+      }
     }
-    const float var = row_sum<WAVE>(sq, red[1], nw) / n;
     const float rstd = 1.0f / sqrtf(var + p.eps);
     if (t == 0) {
       p.mean[row] = mean;
