@@ -12,9 +12,13 @@ Workspaces.  The amax-producing calls take ``workspace``: a device buffer of
 ``fp8_workspace_init``).  Left as ``None``, a fresh workspace is taken from
 torch's allocator for that one call, on the call's stream, which costs one
 small fill kernel; callers that time or capture the path pass their own.
+(Torch hands out memory in the order of the stream that it is taken on, so a
+workspace is taken on the stream that uses it: another stream's memory may
+still be in use by what is pending there.)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -170,12 +174,31 @@ def _rc(x: torch.Tensor, name="x"):
     return rows, cols
 
 
+def _taken_on(stream):
+    """A context whose allocations are in the order of `stream`."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream)
+    return torch.cuda.stream(stream)
+
+
+def _fresh(make, stream):
+    """make()'s workspace for one call on `stream`.  Freed when the call has
+    been enqueued, it goes back to that stream's order."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        raise ValueError("pass a workspace when the stream is a raw handle")
+    with _taken_on(stream):
+        return make()
+
+
 def workspace(device=None, wait_polls: int = 0, stream=None) -> torch.Tensor:
-    """A device workspace for the amax-producing calls, prepared on `stream`
-    by fp8_workspace_init (wait_polls: the one-launch wait's bound, 0 =
-    default).  Calls that may run at the same time need different ones."""
-    dev = torch.device("cuda") if device is None else torch.device(device)
-    ws = torch.empty(WORKSPACE_BYTES, dtype=torch.uint8, device=dev)
+    """A device workspace for the amax-producing calls, taken and prepared on
+    `stream` by fp8_workspace_init (wait_polls: the one-launch wait's bound, 0
+    = default).  Calls that may run at the same time need different ones."""
+    with _taken_on(stream):
+        dev = torch.device("cuda") if device is None else torch.device(device)
+        ws = torch.empty(WORKSPACE_BYTES, dtype=torch.uint8, device=dev)
     fp8_workspace_init(ws, wait_polls, stream)
     return ws
 
@@ -187,19 +210,13 @@ def fp8_workspace_init(ws, wait_polls=0, stream=None):
 
 
 class _Ws:
-    """The call's workspace: the caller's, or a fresh one kept alive until
-    the call's stream has passed it."""
+    """The call's workspace: the caller's, or a fresh one."""
 
     def __init__(self, ws, stream):
         if ws is not None:
             self.ptr = _t(ws, "workspace", _U8, WORKSPACE_BYTES)
             return
-        s = stream if isinstance(stream, torch.cuda.Stream) else None
-        if stream is not None and s is None:
-            raise ValueError("pass a workspace when the stream is a raw handle")
-        self.t = workspace(stream=stream)
-        if s is not None:
-            self.t.record_stream(s)
+        self.t = _fresh(lambda: workspace(stream=stream), stream)
         self.ptr = self.t.data_ptr()
 
 
@@ -502,11 +519,7 @@ def fp8_layernorm_bwd(dy, x, mean, rstd, gamma, dx, dgamma, dbeta, xhat=None, st
     rows, cols = _rc(dy, "dy")
     n = rows * cols
     if workspace is None:
-        workspace = layernorm_workspace(rows, cols, dy.device)
-        if isinstance(stream, torch.cuda.Stream):
-            workspace.record_stream(stream)
-        elif stream is not None:
-            raise ValueError("pass a workspace when the stream is a raw handle")
+        workspace = _fresh(lambda: layernorm_workspace(rows, cols, dy.device), stream)
     if isinstance(x, torch.Tensor) and x.dtype != dx.dtype:
         raise ValueError(f"dx has dtype {dx.dtype}, x {x.dtype}")
     held = None if xhat is None else _held(xhat, "xhat", rows, cols)
@@ -589,11 +602,7 @@ def fp8_moe_sort(expert, experts, pad, offsets, counts, pos, src, stream=None, w
     tokens, k = _rc(expert, "expert")
     n = tokens * k
     if workspace is None:
-        workspace = moe_workspace(n, experts, expert.device)
-        if isinstance(stream, torch.cuda.Stream):
-            workspace.record_stream(stream)
-        elif stream is not None:
-            raise ValueError("pass a workspace when the stream is a raw handle")
+        workspace = _fresh(lambda: moe_workspace(n, experts, expert.device), stream)
     _check("fp8_moe_sort",
            lib().fp8_moe_sort(_t(expert, "expert", _I32, n), tokens, k, experts, pad, src.numel(),
                               _t(offsets, "offsets", _I32, experts + 1),
