@@ -456,6 +456,8 @@ def _check_cast_out(o, name, rows, cols, halves=1):
     their own); returns the reference the C call takes."""
     if o is None:
         return None
+    if not isinstance(o, CastOut):
+        raise TypeError(f"{name} must be a cast_out()")
     data, sc, scale, amax = o._tensors
     _t(data, f"{name}.data", _U8, rows * cols * halves)
     if o.scaling == SCALE_TENSOR:
@@ -469,17 +471,27 @@ def _check_cast_out(o, name, rows, cols, halves=1):
 
 
 def _wants_amax(o):
-    return o is not None and o.scaling == SCALE_TENSOR and o.amax is not None
+    return isinstance(o, CastOut) and o.scaling == SCALE_TENSOR and o.amax is not None
 
 
 def _held(o: Operand, name, rows, cols):
     """Checks a checkpoint of [rows][cols] that a call reads."""
+    if not isinstance(o, Operand):
+        raise TypeError(f"{name} must be an operand()")
     _check_operand(o, name, rows, cols)
     return ctypes.byref(o)
 
 
 def _float_type(x):
-    return TYPE_F32 if x.dtype == torch.float32 else TYPE_BF16
+    return TYPE_F32 if isinstance(x, torch.Tensor) and x.dtype == torch.float32 else TYPE_BF16
+
+
+def _same_type(a, b, name_a, name_b):
+    """Both BF16 (as torch.bfloat16 or as bits) or both FP32, where both are
+    there; what is missing or of another type is _t's to refuse."""
+    if (isinstance(a, torch.Tensor) and isinstance(b, torch.Tensor)
+            and _float_type(a) != _float_type(b)):
+        raise ValueError(f"{name_a} has dtype {a.dtype}, {name_b} {b.dtype}")
 
 
 def fp8_layernorm_fwd(x, gamma, beta, eps, y, mean, rstd, yq=None, xhat=None, stream=None,
@@ -491,8 +503,7 @@ def fp8_layernorm_fwd(x, gamma, beta, eps, y, mean, rstd, yq=None, xhat=None, st
     rows, cols = _rc(x)
     n = rows * cols
     ws = _Ws(workspace, stream) if _wants_amax(yq) else None
-    if isinstance(beta, torch.Tensor) and beta.dtype != gamma.dtype:
-        raise ValueError(f"beta has dtype {beta.dtype}, gamma {gamma.dtype}")
+    _same_type(beta, gamma, "beta", "gamma")
     _check("fp8_layernorm_fwd",
            lib().fp8_layernorm_fwd(_t(x, "x", _BF16_F32, n), _float_type(x),
                                    _t(gamma, "gamma", _BF16_F32, cols),
@@ -520,8 +531,7 @@ def fp8_layernorm_bwd(dy, x, mean, rstd, gamma, dx, dgamma, dbeta, xhat=None, st
     n = rows * cols
     if workspace is None:
         workspace = _fresh(lambda: layernorm_workspace(rows, cols, dy.device), stream)
-    if isinstance(x, torch.Tensor) and x.dtype != dx.dtype:
-        raise ValueError(f"dx has dtype {dx.dtype}, x {x.dtype}")
+    _same_type(dx, x, "dx", "x")
     held = None if xhat is None else _held(xhat, "xhat", rows, cols)
     _check("fp8_layernorm_bwd",
            lib().fp8_layernorm_bwd(
@@ -604,7 +614,8 @@ def fp8_moe_sort(expert, experts, pad, offsets, counts, pos, src, stream=None, w
     if workspace is None:
         workspace = _fresh(lambda: moe_workspace(n, experts, expert.device), stream)
     _check("fp8_moe_sort",
-           lib().fp8_moe_sort(_t(expert, "expert", _I32, n), tokens, k, experts, pad, src.numel(),
+           lib().fp8_moe_sort(_t(expert, "expert", _I32, n), tokens, k, experts, pad,
+                              _length(src, "src"),
                               _t(offsets, "offsets", _I32, experts + 1),
                               _t(counts, "counts", _I32, experts), _t(pos, "pos", _I32, n),
                               _t(src, "src", _I32, 0),
@@ -612,9 +623,16 @@ def fp8_moe_sort(expert, experts, pad, offsets, counts, pos, src, stream=None, w
                                  lib().fp8_moe_workspace_bytes(n, experts)), _stream(stream)))
 
 
+def _length(x, name):
+    if not isinstance(x, torch.Tensor):
+        raise ValueError(f"{name} is required")
+    return x.numel()
+
+
 def _moe_rows_of(pos, src, offsets):
     tokens, k = _rc(pos, "pos")
-    return (tokens, k, src.numel(), offsets.numel() - 1, _t(pos, "pos", _I32, tokens * k),
+    return (tokens, k, _length(src, "src"), _length(offsets, "offsets") - 1,
+            _t(pos, "pos", _I32, tokens * k),
             _t(src, "src", _I32, 0), _t(offsets, "offsets", _I32, 2))
 
 
