@@ -175,7 +175,8 @@ def _rc(x: torch.Tensor, name="x"):
 
 
 def _taken_on(stream):
-    """A context whose allocations are in the order of `stream`."""
+    """A context whose allocations and torch operations are in the order of
+    `stream`."""
     if stream is None:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
@@ -608,7 +609,9 @@ def moe_workspace(n, experts, device=None) -> torch.Tensor:
 def fp8_moe_sort(expert, experts, pad, offsets, counts, pos, src, stream=None, workspace=None):
     """Sort the choices expert[tokens][k] (int32): see fp8_moe_sort in
     include/fp8sg.h.  src holds moe_rows(tokens * k, experts, pad) rows or
-    more.  `workspace`: from moe_workspace(); None takes a fresh one."""
+    more; offsets holds experts + 1 entries, and any further ones repeat the
+    last (the rows in use), which is where the calls that take offsets find
+    it.  `workspace`: from moe_workspace(); None takes a fresh one."""
     tokens, k = _rc(expert, "expert")
     n = tokens * k
     if workspace is None:
@@ -621,6 +624,10 @@ def fp8_moe_sort(expert, experts, pad, offsets, counts, pos, src, stream=None, w
                               _t(src, "src", _I32, 0),
                               _t(workspace, "workspace", _U8,
                                  lib().fp8_moe_workspace_bytes(n, experts)), _stream(stream)))
+    if offsets.numel() > experts + 1:
+        with _taken_on(stream):
+            flat = offsets.view(-1)
+            flat[experts + 1:] = flat[experts:experts + 1]
 
 
 def _length(x, name):
