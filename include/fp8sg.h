@@ -394,7 +394,18 @@ fp8_status_t fp8_convert_f32(const float* x, int64_t n, int32_t fmt, uint8_t* q,
  *   FP8_SCALE_BLOCK_1x128 scale_inv out float [rows][ceil(cols/128)]
  *   FP8_SCALE_MX_1x32     scale_inv out uint8 E8M0 [rows][ceil(cols/32)]
  * data: out uint8 [rows][cols].  Fields that a scaling does not use are
- * ignored. */
+ * ignored.
+ *
+ * Overlap.  Outputs of the row operators must not overlap inputs or each
+ * other, but an output may take the place of an input (the same address) that
+ * has its shape and element type:
+ *   fp8_layernorm_fwd   y_bf16 that of a BF16 x
+ *   fp8_layernorm_bwd   dx that of x, a BF16 dx also that of dy
+ *   fp8_act_fwd         y_bf16 that of h where it is not gated
+ *   fp8_act_bwd         dh that of h, y_bf16 that of dy, and where it is not
+ *                       gated also dh that of dy or y_bf16 that of h
+ * Any other output of rows that starts at the address of an input of rows is
+ * refused (FP8_ERR_UNSUPPORTED). */
 typedef struct {
   uint8_t* data;
   int32_t fmt;             /* fp8_format_t  */

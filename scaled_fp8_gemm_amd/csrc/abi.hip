@@ -13,6 +13,8 @@
 
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "launch.h"
 
 namespace {
@@ -194,6 +196,15 @@ fp8_status_t held_ok(const fp8_operand_t* o, int64_t n) {
   if (!aligned(o->data, 16) || !aligned(o->scale_inv, 4)) return FP8_ERR_ALIGN;
   return FP8_OK;
 }
+// An output that starts where an input does whose elements lie differently
+// would overwrite what is not read yet.
+bool over(const void* out, std::initializer_list<const void*> ins) {
+  if (!out) return false;
+  for (const void* in : ins)
+    if (in == out) return true;
+  return false;
+}
+const void* data_of(const fp8_cast_out_t* o) { return o ? o->data : nullptr; }
 bool type_ok(int32_t t) { return t == FP8_TYPE_BF16 || t == FP8_TYPE_F32; }
 bool act_ok(int32_t act, int32_t gated) {
   return act >= FP8_ACT_GELU && act <= FP8_ACT_SILU && (gated == 0 || gated == 1);
@@ -450,6 +461,9 @@ fp8_status_t fp8_layernorm_fwd(const void* x, int32_t x_type, const void* gamma,
   if (!aligned(x, 16) || !aligned(gamma, 16) || !aligned(beta, 16) || !aligned(y_bf16, 16) ||
       !aligned(mean, 4) || !aligned(rstd, 4) || (amax && !aligned(workspace, 256)))
     return FP8_ERR_ALIGN;
+  if (n > 0 && (over(x_type == FP8_TYPE_F32 ? y_bf16 : nullptr, {x}) || over(data_of(yq), {x}) ||
+                over(data_of(xhat), {x})))
+    return FP8_ERR_UNSUPPORTED;
   fp8sg::NormFwd p;
   p.x = x;
   p.gamma = gamma;
@@ -494,6 +508,9 @@ fp8_status_t fp8_layernorm_bwd(const void* dy_bf16, const void* x, int32_t x_typ
       !aligned(gamma, 16) || !aligned(dx, 16) || !aligned(dgamma, 4) || !aligned(dbeta, 4) ||
       !aligned(workspace, 256))
     return FP8_ERR_ALIGN;
+  if (n > 0 && (over(x_type == FP8_TYPE_F32 ? dx : nullptr, {dy_bf16}) ||
+                (xhat && over(dx, {xhat->data}))))
+    return FP8_ERR_UNSUPPORTED;
   fp8sg::NormBwd p;
   p.dy = static_cast<const uint16_t*>(dy_bf16);
   p.x = x;
@@ -528,6 +545,9 @@ fp8_status_t fp8_act_fwd(const void* h_bf16, int32_t act, int32_t gated, int64_t
   if (amax && !workspace) return FP8_ERR_NULL;
   if (!aligned(h_bf16, 16) || !aligned(y_bf16, 16) || (amax && !aligned(workspace, 256)))
     return FP8_ERR_ALIGN;
+  if (n > 0 && (over(gated ? y_bf16 : nullptr, {h_bf16}) || over(data_of(yq), {h_bf16}) ||
+                over(data_of(ckpt), {h_bf16})))
+    return FP8_ERR_UNSUPPORTED;
   fp8sg::ActFwd p;
   p.h = static_cast<const uint16_t*>(h_bf16);
   p.act = act;
@@ -557,6 +577,10 @@ fp8_status_t fp8_act_bwd(const void* dy_bf16, const void* h_bf16, const fp8_oper
   if (!aligned(dy_bf16, 16) || !aligned(h_bf16, 16) || !aligned(dh_bf16, 16) ||
       !aligned(y_bf16, 16))
     return FP8_ERR_ALIGN;
+  if (n > 0 && (over(gated ? dh_bf16 : nullptr, {dy_bf16}) ||
+                over(gated ? y_bf16 : nullptr, {h_bf16}) ||
+                (ckpt && (over(dh_bf16, {ckpt->data}) || over(y_bf16, {ckpt->data})))))
+    return FP8_ERR_UNSUPPORTED;
   fp8sg::ActBwd p;
   p.dy = static_cast<const uint16_t*>(dy_bf16);
   p.h = static_cast<const uint16_t*>(h_bf16);
@@ -580,6 +604,8 @@ fp8_status_t fp8_checkpoint_save(const void* x_bf16, int64_t rows, int64_t cols,
   const fp8_status_t e = cast_out_ok(ckpt, true, false, rows * cols);
   if (e != FP8_OK) return e;
   if (!aligned(x_bf16, 16)) return FP8_ERR_ALIGN;
+  if (rows * cols > 0 && over(ckpt->data, {x_bf16}))
+    return FP8_ERR_UNSUPPORTED;
   return hip(fp8sg::launch_checkpoint_save(static_cast<const uint16_t*>(x_bf16), rows, cols,
                                            cast_out(ckpt), st(stream)));
 }
@@ -592,6 +618,8 @@ fp8_status_t fp8_checkpoint_load(const fp8_operand_t* ckpt, int64_t rows, int64_
   if (e != FP8_OK) return e;
   if (!have(y_bf16, rows * cols)) return FP8_ERR_NULL;
   if (!aligned(y_bf16, 16)) return FP8_ERR_ALIGN;
+  if (rows * cols > 0 && over(y_bf16, {ckpt->data}))
+    return FP8_ERR_UNSUPPORTED;
   return hip(fp8sg::launch_checkpoint_load(ckpt->data, static_cast<const float*>(ckpt->scale_inv),
                                            ckpt->fmt, rows, cols, static_cast<uint16_t*>(y_bf16),
                                            st(stream)));
@@ -635,6 +663,8 @@ fp8_status_t fp8_moe_dispatch(const void* x_bf16, int64_t tokens, int32_t k, int
   if (!aligned(x_bf16, 16) || !aligned(xs_bf16, 16) || !aligned(pos, 4) || !aligned(src, 4) ||
       !aligned(offsets, 4))
     return FP8_ERR_ALIGN;
+  if (tokens * cols > 0 && (over(xs_bf16, {x_bf16}) || over(data_of(xq), {x_bf16})))
+    return FP8_ERR_UNSUPPORTED;
   const fp8sg::MoeRows p{pos, src, offsets + experts, tokens, rows, k, cols};
   return hip(fp8sg::launch_moe_dispatch(p, static_cast<const uint16_t*>(x_bf16),
                                         static_cast<uint16_t*>(xs_bf16), cast_out(xq),
@@ -649,6 +679,8 @@ fp8_status_t fp8_moe_combine(const void* ys_bf16, const int32_t* pos, const floa
     return FP8_ERR_NULL;
   if (!aligned(ys_bf16, 16) || !aligned(y_bf16, 16) || !aligned(pos, 4) || !aligned(weight, 4))
     return FP8_ERR_ALIGN;
+  if (tokens * cols > 0 && over(y_bf16, {ys_bf16}))
+    return FP8_ERR_UNSUPPORTED;
   const fp8sg::MoeRows p{pos, nullptr, nullptr, tokens, rows, k, cols};
   return hip(fp8sg::launch_moe_combine(p, static_cast<const uint16_t*>(ys_bf16), weight,
                                        static_cast<uint16_t*>(y_bf16), st(stream)));
@@ -669,6 +701,8 @@ fp8_status_t fp8_moe_combine_bwd(const void* dy_bf16, const void* ys_bf16, const
       !aligned(weight, 4) || !aligned(pos, 4) || !aligned(src, 4) || !aligned(offsets, 4) ||
       !aligned(dweight, 4))
     return FP8_ERR_ALIGN;
+  if (rows * cols > 0 && over(dys_bf16, {dy_bf16, ys_bf16}))
+    return FP8_ERR_UNSUPPORTED;
   const fp8sg::MoeRows p{pos, src, offsets + experts, tokens, rows, k, cols};
   return hip(fp8sg::launch_moe_combine_bwd(p, static_cast<const uint16_t*>(dy_bf16),
                                            static_cast<const uint16_t*>(ys_bf16), weight,
