@@ -484,15 +484,15 @@ def _held(o: Operand, name, rows, cols):
 
 
 def _float_type(x):
-    return TYPE_F32 if isinstance(x, torch.Tensor) and x.dtype == torch.float32 else TYPE_BF16
+    return TYPE_F32 if getattr(x, "dtype", None) is torch.float32 else TYPE_BF16
 
 
 def _same_type(a, b, name_a, name_b):
     """Both BF16 (as torch.bfloat16 or as bits) or both FP32, where both are
     there; what is missing or of another type is _t's to refuse."""
-    if (isinstance(a, torch.Tensor) and isinstance(b, torch.Tensor)
-            and _float_type(a) != _float_type(b)):
-        raise ValueError(f"{name_a} has dtype {a.dtype}, {name_b} {b.dtype}")
+    ta, tb = getattr(a, "dtype", None), getattr(b, "dtype", None)
+    if ta is not tb and ta and tb and _float_type(a) != _float_type(b):
+        raise ValueError(f"{name_a} has dtype {ta}, {name_b} {tb}")
 
 
 def fp8_layernorm_fwd(x, gamma, beta, eps, y, mean, rstd, yq=None, xhat=None, stream=None,
