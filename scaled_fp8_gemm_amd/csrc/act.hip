@@ -12,7 +12,8 @@
 // (each half of a gated row has tiles of its own).  All values between load
 // and store are FP32.  Bound by HBM: everything is read and written once.
 // Measured (one MI355X, us):
-//   gated SiLU forward 4096 x 11008, blockwise operand and checkpoint   59  5.4 TB/s
+//   gated SiLU forward 4096 x 11008, blockwise operand and checkpoint   58  5.4 TB/s
+//   the same, per-tensor operand and its amax alone (a launch more)     48  4.7 TB/s
 //   GELU (tanh) backward 4096 x 49152 from the checkpoint, y again     229  6.2 TB/s
 //   checkpoint 8192 x 4096, save and load                               37  5.4 TB/s
 // against 5.1 TB/s of a large copy (one read for each write; these read less

@@ -11,11 +11,13 @@
 // a difference of two large sums).  FP32 rows correct their mean by that of
 // the deviations, which comes with the squares' sum (8192 x 4096, BF16 output:
 // 39.2 us without, 40.0 so, 40.6 with a sum of its own; 4096 x 12288: 56.2,
-// 58.7, 61.0).  Measured (one MI355X, us):
-//   forward 4096 x 12288 BF16, MX operand and checkpoint   49.5 4.1 TB/s
-//   forward 8192 x 4096, BF16 output alone                 26   5.1 TB/s
-//   backward 8192 x 5120 from the checkpoint               47.6 4.4 TB/s
-//   backward 4096 x 12288 from x                           61   5.0 TB/s
+// 58.7, 61.0).  Measured (one MI355X, us, 768 MiB of tensors in turn):
+//   forward 4096 x 12288 BF16, MX operand and checkpoint   49.6 4.1 TB/s
+//   forward 4096 x 12288 BF16, MX operand alone            38.5 3.9 TB/s
+//   forward 8192 x 4096 BF16, BF16 output alone            30.6 4.4 TB/s
+//   backward 8192 x 5120 from the checkpoint               51.1 4.1 TB/s
+//   backward 4096 x 12288 from x                           63.0 4.8 TB/s
+//   backward 2048 x 20480 from x (K = 8, spills)          304   0.8 TB/s
 // against 5.1 TB/s of a large copy.  With two casts the forward pass is bound
 // by its instructions as much as by HBM (19.0 M wave instructions of VALU,
 // 31 us of the chip's issue slots); the backward pass by HBM and, at its end,

@@ -9,13 +9,17 @@
 //   combine     y[t] = sum_j w[t][j] ys[pos[t][j]]
 //   its gradient  dys[pos[t][j]] = w[t][j] dy[t], dw[t][j] = dy[t] . ys[pos[t][j]]
 // (dispatch's gradient is combine without weights.)  The sort is a counting
-// sort of the ids alone, a few microseconds; the rest is bound by HBM and
-// goes by token, so a token's row is read once however many experts take it.
+// sort of the ids alone; the rest is bound by HBM and goes by token, so a
+// token's row is read once however many experts take it.
 // Measured (one MI355X, us):
 //   sort of 16384 choices to 8 experts                  7.4  (16 tokens: 5.0)
-//   dispatch, 8192 tokens x 4096, k 2, blockwise cast  33    4.1 TB/s
-//   combine, 4096 tokens x 4096, k 6                   39.6  5.9 TB/s
+//   sort of 131072 choices to 128 experts              14.5
+//   sort of 10^6 choices to 128 / 1000 experts        104 / 784
+//   dispatch, 8192 tokens x 4096, k 2, blockwise cast  33.5  4.1 TB/s
+//   combine, 4096 tokens x 4096, k 6                   39.8  5.9 TB/s
 //   its gradient, 8192 tokens x 5120, k 2              82    5.1 TB/s
+// Beyond kSelfCount choices every workgroup of the sort adds up all
+// workgroups' counts, which is what 10^6 choices spend their time on.
 #include "tile.h"
 
 namespace fp8sg {
@@ -30,7 +34,10 @@ constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kCounters = 8192;                // LDS counters, several per expert
 constexpr int kMaxSortBlocks = 1024;
 // Up to this many choices every workgroup counts all of them itself, which
-// saves a launch; beyond, a first launch counts.
+// saves a launch; beyond, a first launch counts.  us, without and with the
+// first launch: 16384 choices to 8 experts 7.8 and 11.0, 65536 to 8 11.0 and
+// 11.1, 65536 to 1024 13.0 and 33.9, 131072 to 8 16.3 and 10.6, 131072 to 128
+// 16.9 and 14.5.
 constexpr int64_t kSelfCount = 65536;
 
 // Counters per expert (a power of two, 8 .. 64), so that the lanes of a wave
@@ -198,7 +205,9 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_sort(
 
 // Zeros for the padding rows inside segments, `share` (at most 16) rows per
 // workgroup: few in a small batch, where padding is most of the rows and
-// nothing else runs, 16 where most workgroups find none.
+// nothing else runs, 16 where most workgroups find none.  us of dispatch with
+// 1 and 16 (rows of 4096 columns): 144 rows 3.3 and 8.0, 1920 rows 8.5 and
+// 10.3, 17280 rows with a cast 52 and 37.
 int pad_share(int64_t rows) { return rows <= 1024 ? 1 : 16; }
 __device__ __forceinline__ void zero_padding(const MoeRows& p, int64_t block, int64_t blocks,
                                              int share, uint16_t* xs, const CastOut& xq) {
@@ -440,7 +449,9 @@ hipError_t launch_moe_dispatch(const MoeRows& p, const uint16_t* x, uint16_t* xs
   const int share = pad_share(p.rows);
   const int64_t tb = at_most((p.tokens + kWaves - 1) / kWaves), gx = tb + pad_blocks(p.rows);
   // as many waves as there are slots / 64 while the chip runs them at once
-  // (4 slots a lane: 33.0 against 33.1 us at 8192 tokens x 4096)
+  // (us with 1 and 2 slots a lane, rows of 4096: 16 tokens 3.3 and 3.9, 256
+  // tokens 4.9 and 5.0, 8192 tokens with a cast 66 and 52 when each workgroup
+  // looked for one padding row; 4 slots a lane: 33.0 against 33.1 at 8192)
   const int64_t shares = (p.cols + 511) / 512;
   const int k = shares == 1 || p.tokens * shares <= 4096 ? 1 : 2;
   const int64_t y = (shares + k - 1) / k;
@@ -493,6 +504,9 @@ hipError_t launch_moe_combine_bwd(const MoeRows& rows, const uint16_t* dy, const
   p.stream = 2 * p.cols * (p.tokens + 2 * p.rows) > kStreamBytes;
   const int share = pad_share(p.rows);
   if (p.rows == 0) ys = dy;                    // all choices dropped: read, not used
+  // a wave or a workgroup a token, us: 8192 x 520 14.0 and 21.0, 16384 x 1024
+  // 34 and 42, 4096 x 8192 with k 1 42.5 and 45; but 8192 x 2048 43.5 and 32,
+  // 8192 x 5120 82 and 77.5
   const bool wave = p.tokens >= 2048 || p.cols <= 512;
   const int64_t tb = at_most(wave ? (p.tokens + kWaves - 1) / kWaves : p.tokens);
   const int64_t g = tb + (p.cols > 0 ? pad_blocks(p.rows) : 0);
