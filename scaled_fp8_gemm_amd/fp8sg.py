@@ -180,7 +180,10 @@ def _taken_on(stream):
     if stream is None:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream)
+        handle = _stream(stream)
+        handle = getattr(handle, "value", handle)      # a ctypes pointer's
+        # 0 is the default stream, but ExternalStream's "none given"
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
     return torch.cuda.stream(stream)
 
 

@@ -2,6 +2,7 @@
 torch's memory is handed out in the order of one stream, so the current
 stream's may still be in use by what is pending there."""
 import contextlib
+import ctypes
 
 import pytest
 import torch
@@ -53,6 +54,14 @@ def test_workspaces_are_taken_on_the_calls_stream(taken):
     assert taken == [None] * 2
 
 
+def test_raw_handles(taken, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h: ("external", h))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda: "default")
+    for handle in (0x50, ctypes.c_void_p(0x50), 0, ctypes.c_void_p(0)):
+        F.workspace(stream=handle)
+    assert taken == [("external", 0x50)] * 2 + ["default"] * 2
+
+
 def test_a_raw_handle_needs_a_workspace():
     x, e = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(4, 2, dtype=torch.int32)
     f = torch.zeros(16)
@@ -73,6 +82,8 @@ def test_workspaces_come_from_the_streams_own_memory():
     assert pool(F.workspace(stream=s)) == s.cuda_stream
     assert pool(F.workspace(stream=s.cuda_stream)) == s.cuda_stream
     assert pool(F._Ws(None, s).t) == s.cuda_stream
+    with torch.cuda.stream(s):
+        assert pool(F.workspace(stream=0)) == torch.cuda.default_stream().cuda_stream
     assert pool(F.workspace()) == torch.cuda.current_stream().cuda_stream
 
 
