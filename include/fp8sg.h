@@ -25,7 +25,7 @@
  *   Workspace   The calls that produce an amax (fp8_amax*, fp8_quantize_tensor*
  *               with amax_out, fp8_quantize_tensor_current,
  *               fp8_quantize_pair_current, fp8_gemm_fprop_fused with y_amax,
- *               fp8_layernorm_fwd and fp8_act_fwd with an amax)
+ *               fp8_layernorm_fwd, fp8_rmsnorm_fwd and fp8_act_fwd with an amax)
  *               reduce through a caller-owned device workspace of
  *               FP8_WORKSPACE_BYTES, 256-byte aligned: partial maxima, and
  *               the counters and flags of the one-launch grid-wide maximum.
@@ -56,7 +56,7 @@
  *               FP8_ERR_HIP reports a launch failure.  NaN/inf data are not
  *               errors; they follow the rules above.
  *   Alignment   Data pointers must be 16-byte aligned (FP8_ERR_ALIGN).  The
- *               row operators (layer norm, activations, checkpoints, expert
+ *               row operators (norms, activations, checkpoints, expert
  *               sorting) take rows of any length; their short last tile of
  *               a row has a scale of its own.
  *   Empty       A tensor with zero elements may be passed as NULL; required
@@ -79,7 +79,11 @@ extern "C" {
  * cache lines), and one 128-byte line of settings. */
 #define FP8_WORKSPACE_BYTES 295552
 
-typedef enum { FP8_E4M3 = 0, FP8_E5M2 = 1 } fp8_format_t;
+/* FP4_E2M1 is the 4-bit format of the calls that name it (fp8_quantize_mx4 and
+ * the products under FP8_SCALE_MX_1x32): values 0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives, two codes a byte, the first in the low half, rows of K / 2
+ * bytes.  Other calls refuse it. */
+typedef enum { FP8_E4M3 = 0, FP8_E5M2 = 1, FP4_E2M1 = 4 } fp8_format_t;
 
 typedef enum {
   FP8_SCALE_TENSOR = 0,        /* scale_inv: float[1]                                */
@@ -318,6 +322,37 @@ fp8_status_t fp8_quantize_mx_t(const void* x_bf16, int64_t rows, int64_t cols, i
                                uint8_t* q, uint8_t* scale_e8m0, uint8_t* qT,
                                uint8_t* scale_e8m0_T, void* stream);
 
+/* MX cast to 4 bits ([guide] MXFP8 scaling, with E2M1 elements): blocks of 32
+ * along the contiguous dimension, e = the smallest integer with
+ * amax <= 6 * 2^e (clamped to [-127, 127]), byte = e + 127; an all-zero block
+ * gets 127; a block with inf/NaN gets 0xFF and zero codes;
+ * code = the E2M1 value nearest to x * 2^-e, ties to the even code.
+ *   x_bf16     [rows][cols] BF16, cols % 32 == 0
+ *   q          out uint8 [rows][cols/2] (FP4_E2M1)
+ *   scale_e8m0 out uint8 [rows][cols/32]
+ * Errors: NULL; sizes; alignment. */
+fp8_status_t fp8_quantize_mx4(const void* x_bf16, int64_t rows, int64_t cols, uint8_t* q,
+                              uint8_t* scale_e8m0, void* stream);
+
+/* The same with a transposed, column-wise copy, as fp8_quantize_mx_t:
+ *   x_bf16        [rows][cols] BF16, rows % 32 == 0, cols % 32 == 0
+ *   q             out uint8 [rows][cols/2], nullable (then scale_e8m0 NULL too)
+ *   scale_e8m0    out uint8 [rows][cols/32]
+ *   qT            out uint8 [cols][rows/2], as fp8_quantize_mx4(x^T)
+ *   scale_e8m0_T  out uint8 [cols][rows/32]
+ * Errors: NULL (or q / scale_e8m0 not both given); sizes; alignment. */
+fp8_status_t fp8_quantize_mx4_t(const void* x_bf16, int64_t rows, int64_t cols, uint8_t* q,
+                                uint8_t* scale_e8m0, uint8_t* qT, uint8_t* scale_e8m0_T,
+                                void* stream);
+
+/* What 4-bit codes and their scales stand for: y = code * 2^(byte - 127), NaN
+ * where the byte is 0xFF; exact below 2^128, infinite from there on.
+ *   q          [rows][cols/2] (FP4_E2M1), scale_e8m0 [rows][cols/32], cols % 32 == 0
+ *   y_bf16     out [rows][cols] BF16
+ * Errors: NULL; sizes; alignment. */
+fp8_status_t fp8_dequantize_mx4(const uint8_t* q, const uint8_t* scale_e8m0, int64_t rows,
+                                int64_t cols, void* y_bf16, void* stream);
+
 /* The three GEMMs of a linear layer ([guide] code changes; [snippets] forward
  * and backward flow), FP32 accumulation on MFMA, BF16 output (round to nearest
  * even).  Both operands are K-contiguous ("TN"), so one kernel serves all three:
@@ -401,6 +436,9 @@ fp8_status_t fp8_convert_f32(const float* x, int64_t n, int32_t fmt, uint8_t* q,
  * has its shape and element type:
  *   fp8_layernorm_fwd   y_bf16 that of a BF16 x
  *   fp8_layernorm_bwd   dx that of x, a BF16 dx also that of dy
+ *   fp8_rmsnorm_fwd     h that of x; a BF16 h also that of delta; y_bf16 that
+ *                       of a BF16 x or of delta, where h does not take it
+ *   fp8_rmsnorm_bwd     dx that of h or of dres, a BF16 dx also that of dy
  *   fp8_act_fwd         y_bf16 that of h where it is not gated
  *   fp8_act_bwd         dh that of h, y_bf16 that of dy, and where it is not
  *                       gated also dh that of dy or y_bf16 that of h
@@ -468,6 +506,59 @@ fp8_status_t fp8_layernorm_bwd(const void* dy_bf16, const void* x, int32_t x_typ
                                const void* gamma, int32_t w_type, int64_t rows, int64_t cols,
                                void* dx, float* dgamma, float* dbeta, void* workspace,
                                void* stream);
+
+/* The addition to the residual stream and root-mean-square norm:
+ * h = x + delta (x without delta), rounded to x's type;
+ * rstd = 1 / sqrt(sum_j h_j^2 / cols + eps), xhat = h rstd, y = xhat gamma, in
+ * FP32, from h as rounded.
+ *   x            [rows][cols] of x_type (fp8_type_t), 1 <= cols <= 32768
+ *   delta_bf16   [rows][cols] BF16, nullable
+ *   gamma        [cols] of w_type (fp8_type_t)
+ *   h            out [rows][cols] of x_type, nullable
+ *   y_bf16       out [rows][cols] BF16, nullable
+ *   rstd         out float[rows]
+ *   yq           y cast to FP8, nullable (not FP8_SCALE_BLOCK_128x128)
+ *   xhat         the normalised rows as a checkpoint for fp8_rmsnorm_bwd,
+ *                nullable (FP8_SCALE_BLOCK_1x128)
+ *   workspace    see Workspace; needed where yq has an amax, else may be NULL
+ * At least one of h, y_bf16, yq and xhat must be given (FP8_ERR_NULL).
+ * Errors: NULL; enums and scalings; sizes; eps not a finite number >= 0
+ * (FP8_ERR_SHAPE); alignment. */
+fp8_status_t fp8_rmsnorm_fwd(const void* x, int32_t x_type, const void* delta_bf16,
+                             const void* gamma, int32_t w_type, int64_t rows, int64_t cols,
+                             float eps, void* h, void* y_bf16, float* rstd,
+                             const fp8_cast_out_t* yq, const fp8_cast_out_t* xhat,
+                             void* workspace, void* stream);
+
+/* Bytes of fp8_rmsnorm_bwd's workspace: a row of cols floats for each of its
+ * workgroups, at most 256; 0 for rows = 0 or sizes that the call rejects. */
+int64_t fp8_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
+
+/* Its gradients, with g = dy gamma:
+ *   dx = rstd (g - xhat mean_j(g xhat)) + dres
+ *   dgamma = sum over rows of dy xhat
+ * in FP32; dx is the gradient of x and of delta alike.  The sums over rows have
+ * an order of their own for each size, so that equal calls give equal bits.
+ *   dy_bf16      [rows][cols] BF16
+ *   h            the forward pass's h (its x without delta), of x_type; NULL
+ *                with xhat
+ *   xhat         the checkpoint of the normalised rows instead:
+ *                FP8_SCALE_BLOCK_1x128, scales [rows][ceil(cols/128)]; NULL
+ *                with h
+ *   rstd         float[rows]
+ *   dres         [rows][cols] of x_type: what arrives at h along the stream,
+ *                nullable (zero)
+ *   dx           out [rows][cols] of x_type
+ *   dgamma       out float[cols] (zeros for rows = 0)
+ *   workspace    fp8_rmsnorm_workspace_bytes, 256-byte aligned, any contents
+ *                (not the amax workspace); not shared by calls that may run at
+ *                the same time
+ * Errors: NULL; neither or both of h and xhat (FP8_ERR_NULL); enums; sizes;
+ * alignment. */
+fp8_status_t fp8_rmsnorm_bwd(const void* dy_bf16, const void* h, int32_t x_type,
+                             const float* rstd, const fp8_operand_t* xhat, const void* gamma,
+                             int32_t w_type, const void* dres, int64_t rows, int64_t cols,
+                             void* dx, float* dgamma, void* workspace, void* stream);
 
 /* An activation between two GEMMs: y = act(h), or with gated = 1, where a
  * row of h is [a | u], y = act(a) u.

@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfp8sg.so")
 SOURCES = ["abi.hip", "quant.hip", "gemm.hip", "gemm_mx_k32.hip",
-           "layernorm.hip", "act.hip", "moe.hip"]
+           "layernorm.hip", "act.hip", "moe.hip", "rmsnorm.hip", "quant4.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

@@ -399,6 +399,39 @@ fp8_status_t fp8_quantize_mx(const void* x_bf16, int64_t rows, int64_t cols, int
   return hip(fp8sg::launch_quantize_mx(x_bf16, rows, cols, fmt, q, scale_e8m0, st(stream)));
 }
 
+fp8_status_t fp8_quantize_mx4(const void* x_bf16, int64_t rows, int64_t cols, uint8_t* q,
+                              uint8_t* scale_e8m0, void* stream) {
+  if (!dims_ok(rows, cols) || cols % 32) return FP8_ERR_SHAPE;
+  const int64_t n = rows * cols;
+  if (!have(x_bf16, n) || !have(q, n) || !have(scale_e8m0, n)) return FP8_ERR_NULL;
+  if (!aligned(x_bf16, 16) || !aligned(q, 16)) return FP8_ERR_ALIGN;
+  return hip(fp8sg::launch_quantize_mx4(static_cast<const uint16_t*>(x_bf16), rows, cols, q,
+                                        scale_e8m0, st(stream)));
+}
+
+fp8_status_t fp8_quantize_mx4_t(const void* x_bf16, int64_t rows, int64_t cols, uint8_t* q,
+                                uint8_t* scale_e8m0, uint8_t* qT, uint8_t* scale_e8m0_T,
+                                void* stream) {
+  if (!dims_ok(rows, cols)) return FP8_ERR_SHAPE;
+  const int64_t n = rows * cols;
+  if (!have(x_bf16, n) || !have(qT, n) || !have(scale_e8m0_T, n)) return FP8_ERR_NULL;
+  if ((q == nullptr) != (scale_e8m0 == nullptr)) return FP8_ERR_NULL;
+  if (rows % 32 || cols % 32) return FP8_ERR_SHAPE;
+  if (!aligned(x_bf16, 16) || !aligned(qT, 16) || !aligned(q, 16)) return FP8_ERR_ALIGN;
+  return hip(fp8sg::launch_quantize_mx4_t(static_cast<const uint16_t*>(x_bf16), rows, cols, q,
+                                          scale_e8m0, qT, scale_e8m0_T, st(stream)));
+}
+
+fp8_status_t fp8_dequantize_mx4(const uint8_t* q, const uint8_t* scale_e8m0, int64_t rows,
+                                int64_t cols, void* y_bf16, void* stream) {
+  if (!dims_ok(rows, cols) || cols % 32) return FP8_ERR_SHAPE;
+  const int64_t n = rows * cols;
+  if (!have(q, n) || !have(scale_e8m0, n) || !have(y_bf16, n)) return FP8_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(y_bf16, 16)) return FP8_ERR_ALIGN;
+  return hip(fp8sg::launch_dequantize_mx4(q, scale_e8m0, rows, cols,
+                                          static_cast<uint16_t*>(y_bf16), st(stream)));
+}
+
 fp8_status_t fp8_gemm_fprop(const fp8_operand_t* x, const fp8_operand_t* w, int64_t M, int64_t N,
                             int64_t K, void* y_bf16, void* stream) {
   return gemm(x, w, M, N, K, y_bf16, stream);
@@ -529,6 +562,94 @@ fp8_status_t fp8_layernorm_bwd(const void* dy_bf16, const void* x, int32_t x_typ
   p.dbeta = dbeta;
   p.part = static_cast<float*>(workspace);
   return hip(fp8sg::launch_layernorm_bwd(p, st(stream)));
+}
+
+fp8_status_t fp8_rmsnorm_fwd(const void* x, int32_t x_type, const void* delta_bf16,
+                             const void* gamma, int32_t w_type, int64_t rows, int64_t cols,
+                             float eps, void* h, void* y_bf16, float* rstd,
+                             const fp8_cast_out_t* yq, const fp8_cast_out_t* xhat,
+                             void* workspace, void* stream) {
+  if (!gamma) return FP8_ERR_NULL;
+  if (!type_ok(x_type) || !type_ok(w_type)) return FP8_ERR_UNSUPPORTED;
+  if (!norm_dims_ok(rows, cols) || !(eps >= 0.0f && eps <= 3.402823466e+38f)) return FP8_ERR_SHAPE;
+  const int64_t n = rows * cols;
+  if (!have(x, n) || !have(rstd, n) || (!h && !y_bf16 && !yq && !xhat && n > 0))
+    return FP8_ERR_NULL;
+  fp8_status_t e = cast_out_ok(yq, false, true, n);
+  if (e == FP8_OK) e = cast_out_ok(xhat, true, false, n);
+  if (e != FP8_OK) return e;
+  float* amax = amax_of(yq);
+  if (amax && !workspace) return FP8_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(delta_bf16, 16) || !aligned(gamma, 16) || !aligned(h, 16) ||
+      !aligned(y_bf16, 16) || !aligned(rstd, 4) || (amax && !aligned(workspace, 256)))
+    return FP8_ERR_ALIGN;
+  const bool f32 = x_type == FP8_TYPE_F32;
+  if (n > 0 && (over(f32 ? h : nullptr, {delta_bf16}) || over(f32 ? y_bf16 : nullptr, {x}) ||
+                over(h, {y_bf16}) || over(data_of(yq), {x, delta_bf16}) ||
+                over(data_of(xhat), {x, delta_bf16})))
+    return FP8_ERR_UNSUPPORTED;
+  fp8sg::RmsFwd p;
+  p.x = x;
+  p.delta = static_cast<const uint16_t*>(delta_bf16);
+  p.gamma = gamma;
+  p.x_type = x_type;
+  p.w_type = w_type;
+  p.rows = rows;
+  p.cols = (int)cols;
+  p.eps = eps;
+  p.h = h;
+  p.y = static_cast<uint16_t*>(y_bf16);
+  p.rstd = rstd;
+  p.yq = cast_out(yq);
+  p.xhat = cast_out(xhat);
+  p.amax = amax;
+  p.part = amax ? wsp(workspace) : nullptr;
+  return hip(fp8sg::launch_rmsnorm_fwd(p, st(stream)));
+}
+
+int64_t fp8_rmsnorm_workspace_bytes(int64_t rows, int64_t cols) {
+  if (!norm_dims_ok(rows, cols)) return 0;
+  return (int64_t)fp8sg::layernorm_bwd_partials(rows) * cols * 4;
+}
+
+fp8_status_t fp8_rmsnorm_bwd(const void* dy_bf16, const void* h, int32_t x_type,
+                             const float* rstd, const fp8_operand_t* xhat, const void* gamma,
+                             int32_t w_type, const void* dres, int64_t rows, int64_t cols,
+                             void* dx, float* dgamma, void* workspace, void* stream) {
+  if (!gamma || !dgamma) return FP8_ERR_NULL;
+  if (!type_ok(x_type) || !type_ok(w_type)) return FP8_ERR_UNSUPPORTED;
+  if (!norm_dims_ok(rows, cols)) return FP8_ERR_SHAPE;
+  const int64_t n = rows * cols;
+  if (!have(dy_bf16, n) || !have(dx, n) || !have(rstd, n) || !have(workspace, n))
+    return FP8_ERR_NULL;
+  if (xhat ? h != nullptr : !have(h, n)) return FP8_ERR_NULL;
+  if (xhat) {
+    const fp8_status_t e = held_ok(xhat, n);
+    if (e != FP8_OK) return e;
+  }
+  if (!aligned(dy_bf16, 16) || !aligned(h, 16) || !aligned(rstd, 4) || !aligned(gamma, 16) ||
+      !aligned(dres, 16) || !aligned(dx, 16) || !aligned(dgamma, 4) || !aligned(workspace, 256))
+    return FP8_ERR_ALIGN;
+  if (n > 0 && (over(x_type == FP8_TYPE_F32 ? dx : nullptr, {dy_bf16}) ||
+                (xhat && over(dx, {xhat->data}))))
+    return FP8_ERR_UNSUPPORTED;
+  fp8sg::RmsBwd p;
+  p.dy = static_cast<const uint16_t*>(dy_bf16);
+  p.x = h;
+  p.rstd = rstd;
+  p.xhat = xhat ? xhat->data : nullptr;
+  p.xhat_scale = xhat ? static_cast<const float*>(xhat->scale_inv) : nullptr;
+  p.xhat_fmt = xhat ? xhat->fmt : 0;
+  p.gamma = gamma;
+  p.dres = dres;
+  p.x_type = x_type;
+  p.w_type = w_type;
+  p.rows = rows;
+  p.cols = (int)cols;
+  p.dx = dx;
+  p.dgamma = dgamma;
+  p.part = static_cast<float*>(workspace);
+  return hip(fp8sg::launch_rmsnorm_bwd(p, st(stream)));
 }
 
 fp8_status_t fp8_act_fwd(const void* h_bf16, int32_t act, int32_t gated, int64_t rows,

@@ -88,6 +88,13 @@ hipError_t launch_quantize_block(const void* x, int64_t rows, int64_t cols, int 
                                  uint8_t* q, float* scale_inv, hipStream_t s);
 hipError_t launch_quantize_mx(const void* x, int64_t rows, int64_t cols, int fmt, uint8_t* q,
                               uint8_t* e8m0, hipStream_t s);
+// E2M1 codes in blocks of 32 (rows % 32 == 0 along columns), and back.
+hipError_t launch_quantize_mx4(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* q,
+                               uint8_t* e8m0, hipStream_t s);
+hipError_t launch_quantize_mx4_t(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* q,
+                                 uint8_t* e8m0, uint8_t* qT, uint8_t* e8m0T, hipStream_t s);
+hipError_t launch_dequantize_mx4(const uint8_t* q, const uint8_t* e8m0, int64_t rows, int64_t cols,
+                                 uint16_t* y, hipStream_t s);
 // Row-wise copy (optional) and transposed column-wise copy; kind 0: 1x128
 // blocks, 1: 128x128 blocks, 2: MX 1x32 blocks.
 hipError_t launch_quantize_t(const void* x, int64_t rows, int64_t cols, int fmt, int kind,
@@ -157,6 +164,42 @@ struct NormBwd {
 // The most workgroups of the backward pass, each with one row of partial sums.
 int layernorm_bwd_partials(int64_t rows);
 hipError_t launch_layernorm_bwd(const NormBwd& p, hipStream_t s);
+
+// The residual's addition and root-mean-square norm, rows of 1 .. kMaxNormCols.
+struct RmsFwd {
+  const void* x;
+  const uint16_t* delta;  // BF16, or NULL
+  const void* gamma;
+  int x_type, w_type;
+  int64_t rows;
+  int cols;
+  float eps;
+  void* h;                // x + delta in x's type, or NULL
+  uint16_t* y;            // BF16, or NULL
+  float* rstd;
+  CastOut yq, xhat;       // xhat: kCastBlock or absent
+  bool stream = false;
+  float* amax;            // amax of y (with yq per tensor), or NULL
+  uint32_t* part;         // its partial maxima (the caller's workspace)
+};
+hipError_t launch_rmsnorm_fwd(const RmsFwd& p, hipStream_t s);
+struct RmsBwd {
+  const uint16_t* dy;
+  const void* x;          // NULL: the normalised rows come from xhat
+  const float* rstd;
+  const uint8_t* xhat;
+  const float* xhat_scale;
+  int xhat_fmt;
+  const void* gamma;
+  const void* dres;       // of x_type, or NULL
+  int x_type, w_type;     // x_type: of x, dres and dx
+  int64_t rows;
+  int cols;
+  void* dx;
+  float* dgamma;
+  float* part;            // layernorm_bwd_partials() rows of cols floats
+};
+hipError_t launch_rmsnorm_bwd(const RmsBwd& p, hipStream_t s);
 
 // Activations between two GEMMs, and their 8-bit checkpoints.
 enum : int { kActGelu = 0, kActGeluTanh = 1, kActSilu = 2 };

@@ -61,4 +61,33 @@ inline BwdShape bwd_shape(int64_t rows, int64_t cols, bool held, bool f32) {
   return b;
 }
 
+// Root-mean-square norm.  Forward: as layer norm, with the row's two inputs
+// in the registers of beta and the mean's passes; above 16384 columns four
+// slots to each of 1024 threads.
+constexpr int rms_fwd_waves(int k, bool f32) {
+  return k == 1 ? 32 : k == 2 || k == 4 || (k == 3 && !f32) ? 16 : 8;
+}
+inline RowShape rms_row_shape(int64_t rows, int64_t cols) {
+  const RowShape r = row_shape(rows, cols);
+  return r.k == 8 ? RowShape{4, 1024, false} : r;
+}
+
+// Backward: as layer norm, with one sum per column instead of two, and the
+// stream's gradient beside the row; 128 registers are enough for two slots of
+// either type.
+constexpr int kRmsBwdThreads = 1024;
+inline BwdShape rms_bwd_shape(int64_t rows, int64_t cols) {
+  const int slots = (int)((cols + 7) / 8);
+  BwdShape b;
+  const int64_t even = rows > 256 ? (rows + 255) / 256 : 1;
+  // one slot a thread where all rows are in registers at once even so
+  b.k = slots <= 64 || even * round_up64(slots) <= 1024 ? 1 : slots <= 2048 ? 2 : 4;
+  b.nt = round_up64((slots + b.k - 1) / b.k);
+  const int64_t most = kRmsBwdThreads / b.nt;
+  b.groups = (int)(even < most ? even : most);
+  const int64_t need = (rows + b.groups - 1) / b.groups;
+  b.grid = (int)(need < 256 ? need : 256);
+  return b;
+}
+
 }  // namespace fp8sg

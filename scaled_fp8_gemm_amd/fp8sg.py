@@ -26,6 +26,7 @@ import torch
 
 E4M3 = 0
 E5M2 = 1
+FP4_E2M1 = 4
 SCALE_TENSOR = 0
 SCALE_BLOCK_1x128 = 1
 SCALE_BLOCK_128x128 = 2
@@ -100,6 +101,12 @@ def lib():
             "fp8_layernorm_fwd": [vp, i32, vp, vp, i32, i64, i64, ctypes.c_float, vp, vp, vp, vp,
                                   vp, vp, vp],
             "fp8_layernorm_bwd": [vp, vp, i32, vp, vp, vp, vp, i32, i64, i64, vp, vp, vp, vp, vp],
+            "fp8_quantize_mx4": [vp, i64, i64, vp, vp, vp],
+            "fp8_quantize_mx4_t": [vp, i64, i64, vp, vp, vp, vp, vp],
+            "fp8_dequantize_mx4": [vp, vp, i64, i64, vp, vp],
+            "fp8_rmsnorm_fwd": [vp, i32, vp, vp, i32, i64, i64, ctypes.c_float, vp, vp, vp, vp,
+                                vp, vp, vp],
+            "fp8_rmsnorm_bwd": [vp, vp, i32, vp, vp, vp, i32, vp, i64, i64, vp, vp, vp, vp],
             "fp8_act_fwd": [vp, i32, i32, i64, i64, vp, vp, vp, vp, vp],
             "fp8_act_bwd": [vp, vp, vp, i32, i32, i64, i64, vp, vp, vp],
             "fp8_checkpoint_save": [vp, i64, i64, vp, vp],
@@ -114,6 +121,7 @@ def lib():
             fn.argtypes = args
             fn.restype = ctypes.c_int
         for name, args in {"fp8_layernorm_workspace_bytes": [i64, i64],
+                           "fp8_rmsnorm_workspace_bytes": [i64, i64],
                            "fp8_moe_rows": [i64, i32, i32],
                            "fp8_moe_workspace_bytes": [i64, i32]}.items():
             fn = getattr(L, name)
@@ -372,6 +380,41 @@ def fp8_quantize_mx_t(x, fmt, q, scale_e8m0, qT, scale_e8m0_T, stream=None):
                                    _stream(stream)))
 
 
+def fp8_quantize_mx4(x, q, scale_e8m0, stream=None):
+    """x [rows][cols] BF16 to 4 bits (E2M1) in blocks of 32 along its rows:
+    q [rows][cols / 2], two codes a byte, and the blocks' E8M0 scales."""
+    rows, cols = _rc(x)
+    n = rows * cols
+    _check("fp8_quantize_mx4",
+           lib().fp8_quantize_mx4(_t(x, "x", _BF16, n), rows, cols, _t(q, "q", _U8, n // 2),
+                                  _t(scale_e8m0, "scale_e8m0", _U8, rows * _blocks(cols, 32)),
+                                  _stream(stream)))
+
+
+def fp8_quantize_mx4_t(x, q, scale_e8m0, qT, scale_e8m0_T, stream=None):
+    """fp8_quantize_mx4 of x (q and scale_e8m0 None: not) and of x^T."""
+    rows, cols = _rc(x)
+    n = rows * cols
+    _check("fp8_quantize_mx4_t",
+           lib().fp8_quantize_mx4_t(_t(x, "x", _BF16, n), rows, cols,
+                                    _t(q, "q", _U8, n // 2, True),
+                                    _t(scale_e8m0, "scale_e8m0", _U8, rows * _blocks(cols, 32),
+                                       True),
+                                    _t(qT, "qT", _U8, n // 2),
+                                    _t(scale_e8m0_T, "scale_e8m0_T", _U8,
+                                       cols * _blocks(rows, 32)),
+                                    _stream(stream)))
+
+
+def fp8_dequantize_mx4(q, scale_e8m0, rows, cols, y, stream=None):
+    """4-bit codes and their scales back to y [rows][cols] BF16."""
+    n = rows * cols
+    _check("fp8_dequantize_mx4",
+           lib().fp8_dequantize_mx4(_t(q, "q", _U8, n // 2),
+                                    _t(scale_e8m0, "scale_e8m0", _U8, rows * _blocks(cols, 32)),
+                                    rows, cols, _t(y, "y", _BF16, n), _stream(stream)))
+
+
 # ------------------------------------------------------------ GEMMs
 def operand(data, fmt, scaling, scale_inv) -> Operand:
     """The operand holds the two tensors as well as their addresses, so that
@@ -545,6 +588,59 @@ def fp8_layernorm_bwd(dy, x, mean, rstd, gamma, dx, dgamma, dbeta, xhat=None, st
                _float_type(gamma), rows, cols, _t(dx, "dx", _BF16_F32, n),
                _t(dgamma, "dgamma", _F32, cols), _t(dbeta, "dbeta", _F32, cols),
                _t(workspace, "workspace", _U8, lib().fp8_layernorm_workspace_bytes(rows, cols)),
+               _stream(stream)))
+
+
+def fp8_rmsnorm_fwd(x, delta, gamma, eps, h, y, rstd, yq=None, xhat=None, stream=None,
+                    workspace=None):
+    """h = x + delta (BF16, or None) in x's type (BF16 or FP32), and the
+    root-mean-square norm of h's rows with gamma: h and y (BF16), either None
+    where it is not wanted, the rows' rstd, y cast to FP8 (`yq`) and the
+    normalised rows in 8 bits for the backward pass (`xhat`), both from
+    cast_out()."""
+    rows, cols = _rc(x)
+    n = rows * cols
+    ws = _Ws(workspace, stream) if _wants_amax(yq) else None
+    _same_type(h, x, "h", "x")
+    _check("fp8_rmsnorm_fwd",
+           lib().fp8_rmsnorm_fwd(_t(x, "x", _BF16_F32, n), _float_type(x),
+                                 _t(delta, "delta", _BF16, n, True),
+                                 _t(gamma, "gamma", _BF16_F32, cols), _float_type(gamma), rows,
+                                 cols, eps, _t(h, "h", _BF16_F32, n, True),
+                                 _t(y, "y", _BF16, n, True), _t(rstd, "rstd", _F32, rows),
+                                 _check_cast_out(yq, "yq", rows, cols),
+                                 _check_cast_out(xhat, "xhat", rows, cols),
+                                 ws.ptr if ws else None, _stream(stream)))
+
+
+def rmsnorm_workspace(rows, cols, device=None) -> torch.Tensor:
+    """fp8_rmsnorm_bwd's workspace for these sizes (any contents)."""
+    dev = torch.device("cuda") if device is None else torch.device(device)
+    return torch.empty(max(4, lib().fp8_rmsnorm_workspace_bytes(rows, cols)),
+                       dtype=torch.uint8, device=dev)
+
+
+def fp8_rmsnorm_bwd(dy, h, rstd, gamma, dres, dx, dgamma, xhat=None, stream=None,
+                    workspace=None):
+    """Gradients of fp8_rmsnorm_fwd from its h (its x without delta), or from
+    the checkpoint `xhat` (an operand(); h is then None).  dres: what arrives
+    at h along the stream, of dx's type, or None.  `workspace`: from
+    rmsnorm_workspace(); None takes a fresh one for this call."""
+    rows, cols = _rc(dy, "dy")
+    n = rows * cols
+    if workspace is None:
+        workspace = _fresh(lambda: rmsnorm_workspace(rows, cols, dy.device), stream)
+    _same_type(dx, h, "dx", "h")
+    _same_type(dx, dres, "dx", "dres")
+    held = None if xhat is None else _held(xhat, "xhat", rows, cols)
+    _check("fp8_rmsnorm_bwd",
+           lib().fp8_rmsnorm_bwd(
+               _t(dy, "dy", _BF16, n), _t(h, "h", _BF16_F32, n, held is not None),
+               _float_type(dx), _t(rstd, "rstd", _F32, rows), held,
+               _t(gamma, "gamma", _BF16_F32, cols), _float_type(gamma),
+               _t(dres, "dres", _BF16_F32, n, True), rows, cols, _t(dx, "dx", _BF16_F32, n),
+               _t(dgamma, "dgamma", _F32, cols),
+               _t(workspace, "workspace", _U8, lib().fp8_rmsnorm_workspace_bytes(rows, cols)),
                _stream(stream)))
 
 
