@@ -102,7 +102,8 @@ typedef enum {
 } fp8_status_t;
 
 /* One quantised GEMM operand: `data` is FP8 [rows][K] row-major (K contiguous,
- * K = the GEMM's contraction length), with its dequantisation scales. */
+ * K = the GEMM's contraction length; FP4_E2M1: [rows][K/2]), with its
+ * dequantisation scales. */
 typedef struct {
   const uint8_t* data;
   int32_t fmt;             /* fp8_format_t  */
@@ -364,6 +365,8 @@ fp8_status_t fp8_dequantize_mx4(const uint8_t* q, const uint8_t* scale_e8m0, int
  *   block  x block :  sum_b sa(i,b) * sb(j,b) * sum_{t in block b} a(i,t) b(j,t)
  *                     (each operand 1x128 or 128x128; 128-wide blocks along t)
  *   MX     x MX    :  sum_t a(i,t) 2^ea(i,t/32) * b(j,t) 2^eb(j,t/32)
+ * Under MX the second operand, or both, may be FP4_E2M1 (the first alone:
+ * FP8_ERR_UNSUPPORTED): 4-bit weights with 8- or 4-bit rows, the same sums.
  * Shape rules: sizes >= 0; contraction % 16 == 0 (FP8_ERR_ALIGN); block
  * operands need contraction % 128 == 0 and, for 128x128, rows % 128 == 0; MX
  * needs contraction % 32 == 0; contraction <= 2^23 (FP8_ERR_SHAPE).  Mixed families are
@@ -411,6 +414,46 @@ fp8_status_t fp8_gemm_fprop_fused(const fp8_operand_t* x, const fp8_operand_t* w
 fp8_status_t fp8_gemm_wgrad_f32(const fp8_operand_t* dyT, const fp8_operand_t* xT, int64_t M,
                                 int64_t N, int64_t K, float* dw_f32, int32_t accumulate,
                                 void* stream);
+
+/* The three GEMMs of a layer of experts, on rows sorted by expert as
+ * fp8_moe_sort and fp8_moe_dispatch leave them: segment e is the rows
+ * [offsets[e], offsets[e+1]), read on the device, so nothing waits for their
+ * sizes and the calls can be captured.  FP32 accumulation, BF16 output.
+ *   fprop  y[r][N]   = sum_k x[r][K](r,k)  * w[e][N][K](n,k)    r in segment e
+ *   dgrad  dx[r][K]  = sum_n dy[r][N](r,n) * wT[e][K][N](k,n)   r in segment e
+ *   wgrad  dw[e][N][K] = sum_r dyT[N][rows](n,r) * xT[K][rows](k,r)
+ *                                              over the rows r of segment e
+ *   offsets   int32 [experts + 1], not decreasing; what lies outside [0, rows)
+ *             is cut off.  experts 1 .. 1024
+ *   rows      rows of x, dy, y, dx and row length of dyT, xT
+ *   x, dy     [rows][K] ([rows][N]): per-tensor, 1x128 or MX scales
+ *   w, wT     [experts][N][K] ([experts][K][N]), one expert after the other
+ *             with its scales: float[experts] per tensor, and 1x128, 128x128
+ *             (the outputs' number % 128 == 0) or MX scales of experts * N (K)
+ *             rows.  MX: may be FP4_E2M1, and with it x or dy
+ *   dyT, xT   per-tensor, 1x128 or MX scales, 8 bits (the transposed casts of
+ *             the sorted rows: a multiple of 128 to a segment keeps the tiles
+ *             of one expert apart)
+ * Rows of y and dx that are in no segment are left alone.  An expert without
+ * rows gets dw = 0 (or keeps it, accumulating).
+ * Scaling of the outputs, and shape rules for the contraction, as fp8_gemm_*;
+ * wgrad: rows and all offsets % 16 == 0, block and MX % 128 == 0 (an offset
+ * that is not is rounded down).
+ * Errors: as fp8_gemm_*; NULL offsets; experts. */
+fp8_status_t fp8_gemm_grouped_fprop(const fp8_operand_t* x, const fp8_operand_t* w,
+                                    const int32_t* offsets, int32_t experts, int64_t rows,
+                                    int64_t N, int64_t K, void* y_bf16, void* stream);
+fp8_status_t fp8_gemm_grouped_dgrad(const fp8_operand_t* dy, const fp8_operand_t* wT,
+                                    const int32_t* offsets, int32_t experts, int64_t rows,
+                                    int64_t N, int64_t K, void* dx_bf16, void* stream);
+fp8_status_t fp8_gemm_grouped_wgrad(const fp8_operand_t* dyT, const fp8_operand_t* xT,
+                                    const int32_t* offsets, int32_t experts, int64_t rows,
+                                    int64_t N, int64_t K, void* dw_bf16, void* stream);
+/* wgrad with an FP32 result, optionally accumulated, as fp8_gemm_wgrad_f32. */
+fp8_status_t fp8_gemm_grouped_wgrad_f32(const fp8_operand_t* dyT, const fp8_operand_t* xT,
+                                        const int32_t* offsets, int32_t experts, int64_t rows,
+                                        int64_t N, int64_t K, float* dw_f32, int32_t accumulate,
+                                        void* stream);
 
 /* The cast's rounding step alone: q[i] = cast(x[i]) for FP32 inputs (no
  * scaling).  Every quantise kernel above rounds through the same device

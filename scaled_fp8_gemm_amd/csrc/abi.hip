@@ -37,6 +37,18 @@ hipStream_t st(void* s) { return reinterpret_cast<hipStream_t>(s); }
 bool have(const void* p, int64_t elems) { return p != nullptr || elems == 0; }
 
 bool is_block(int32_t sc) { return sc == FP8_SCALE_BLOCK_1x128 || sc == FP8_SCALE_BLOCK_128x128; }
+bool is_fp4(const fp8_operand_t* o) { return o->fmt == FP4_E2M1; }
+
+// The formats and scalings of a GEMM's operands: tensor (0), block (1) or MX
+// (2), or -1.  4-bit operands: the second or both, under MX.
+int gemm_mode(const fp8_operand_t* a, const fp8_operand_t* b) {
+  if (!(fmt_ok(a->fmt) || is_fp4(a)) || !(fmt_ok(b->fmt) || is_fp4(b))) return -1;
+  if (is_fp4(a) && !is_fp4(b)) return -1;
+  if (is_fp4(b) && b->scaling != FP8_SCALE_MX_1x32) return -1;
+  if (a->scaling == FP8_SCALE_TENSOR && b->scaling == FP8_SCALE_TENSOR) return 0;
+  if (is_block(a->scaling) && is_block(b->scaling)) return 1;
+  return a->scaling == FP8_SCALE_MX_1x32 && b->scaling == FP8_SCALE_MX_1x32 ? 2 : -1;
+}
 
 // The caller's workspace: FP8_WORKSPACE_BYTES of device memory, 256-byte
 // aligned (the grid-wide maximum's words sit in whole 128-byte lines).
@@ -59,28 +71,17 @@ fp8_status_t gemm(const fp8_operand_t* a, const fp8_operand_t* b, int64_t rows_a
                   const Fused& fu = Fused()) {
   const bool fused = fu.cq != nullptr || fu.amax != nullptr;
   if (!a || !b) return FP8_ERR_NULL;
-  if (!fmt_ok(a->fmt) || !fmt_ok(b->fmt) || (fu.cq && !fmt_ok(fu.q_fmt)))
-    return FP8_ERR_UNSUPPORTED;
-  if (a->scaling < FP8_SCALE_TENSOR || a->scaling > FP8_SCALE_MX_1x32 ||
-      b->scaling < FP8_SCALE_TENSOR || b->scaling > FP8_SCALE_MX_1x32)
-    return FP8_ERR_UNSUPPORTED;
-  int mode;
-  if (a->scaling == FP8_SCALE_TENSOR && b->scaling == FP8_SCALE_TENSOR)
-    mode = 0;
-  else if (is_block(a->scaling) && is_block(b->scaling))
-    mode = 1;
-  else if (a->scaling == FP8_SCALE_MX_1x32 && b->scaling == FP8_SCALE_MX_1x32)
-    mode = 2;
-  else
-    return FP8_ERR_UNSUPPORTED;
+  const int mode = gemm_mode(a, b);
+  if (mode < 0 || (fu.cq && !fmt_ok(fu.q_fmt))) return FP8_ERR_UNSUPPORTED;
   if (!dims_ok(rows_a, kc) || !dims_ok(rows_b, kc)) return FP8_ERR_SHAPE;
   if (kc > kMaxContraction) return FP8_ERR_SHAPE;
   const int64_t nc = rows_a * rows_b;
   // the output may be NULL when it is empty, or in the fused call when the
   // FP8 copy is written instead
   const bool c_ok = have(c, nc) || fu.cq != nullptr;
+  const int64_t ns = is_fp4(b) && kc == 0 ? 0 : nc;   // no blocks, no scales
   if (!have(a->data, rows_a * kc) || !have(b->data, rows_b * kc) || !c_ok ||
-      !have(a->scale_inv, nc) || !have(b->scale_inv, nc) || (fu.cq && !fu.q_scale) ||
+      !have(a->scale_inv, ns) || !have(b->scale_inv, ns) || (fu.cq && !fu.q_scale) ||
       (fu.amax && !fu.ws))
     return FP8_ERR_NULL;
   if (mode == 1) {
@@ -98,7 +99,7 @@ fp8_status_t gemm(const fp8_operand_t* a, const fp8_operand_t* b, int64_t rows_a
     return FP8_ERR_ALIGN;
   if (mode != 2 && (!aligned(a->scale_inv, 4) || !aligned(b->scale_inv, 4)))
     return FP8_ERR_ALIGN;
-  GemmProblem p;
+  fp8sg::SegProblem p;
   p.A = a->data;
   p.B = b->data;
   p.sa = a->scale_inv;
@@ -119,7 +120,66 @@ fp8_status_t gemm(const fp8_operand_t* a, const fp8_operand_t* b, int64_t rows_a
   p.mode = mode;
   p.bra = a->scaling == FP8_SCALE_BLOCK_128x128 ? 128 : 1;
   p.brb = b->scaling == FP8_SCALE_BLOCK_128x128 ? 128 : 1;
-  return hip(fp8sg::launch_gemm(p, st(stream)));
+  return hip(is_fp4(b) ? fp8sg::launch_gemm_fp4(p, st(stream)) : fp8sg::launch_gemm(p, st(stream)));
+}
+
+// Products by expert.  rows: of the sorted tokens.  Not depth: C[rows][n] =
+// A[rows][k] in segments times B[experts][n][k]; depth: C[experts][n][k] =
+// A[n][rows] . B[k][rows] over the segments of rows.
+fp8_status_t grouped(const fp8_operand_t* a, const fp8_operand_t* b, const int32_t* offsets,
+                     int32_t experts, int64_t rows, int64_t n, int64_t k, void* c, bool depth,
+                     int out, void* stream) {
+  if (!a || !b || !offsets) return FP8_ERR_NULL;
+  const int mode = gemm_mode(a, b);
+  if (mode < 0 || a->scaling == FP8_SCALE_BLOCK_128x128 ||
+      (depth && (is_fp4(b) || b->scaling == FP8_SCALE_BLOCK_128x128)))
+    return FP8_ERR_UNSUPPORTED;
+  const int64_t kc = depth ? rows : k;         // what is contracted, a row's length
+  if (!dims_ok(rows, n) || !dims_ok(n, k) || kc > kMaxContraction || experts < 1 ||
+      experts > fp8sg::kMaxExperts)
+    return FP8_ERR_SHAPE;
+  const auto tiles = [](int64_t v, int64_t t) { return (v + t - 1) / t; };
+  if ((depth ? (tiles(n, 256) * tiles(k, 256) + 7) * experts
+             : (rows / 128 + experts) * tiles(n, 256) + 7) > fp8sg::kMaxGrid)
+    return FP8_ERR_SHAPE;
+  const int64_t na = depth ? n * rows : rows * k, nb = depth ? k * rows : n * k;
+  const int64_t nc = depth ? n * k : rows * n;
+  const int64_t ns = mode != 0 && kc == 0 ? 0 : nc;   // no blocks, no scales
+  if (!have(a->data, na) || !have(b->data, nb) || !have(c, nc) || !have(a->scale_inv, ns) ||
+      !have(b->scale_inv, ns))
+    return FP8_ERR_NULL;
+  if ((mode == 1 || (mode == 2 && depth)) && kc % 128) return FP8_ERR_SHAPE;
+  if (b->scaling == FP8_SCALE_BLOCK_128x128 && n % 128) return FP8_ERR_SHAPE;
+  if (mode == 2 && kc % 32) return FP8_ERR_SHAPE;
+  if (kc % 16) return FP8_ERR_ALIGN;
+  if (!aligned(a->data, 16) || !aligned(b->data, 16) || !aligned(c, 16) || !aligned(offsets, 4))
+    return FP8_ERR_ALIGN;
+  if ((mode != 2 || depth) && (!aligned(a->scale_inv, 4) || !aligned(b->scale_inv, 4)))
+    return FP8_ERR_ALIGN;
+  fp8sg::SegProblem p;
+  p.A = a->data;
+  p.B = b->data;
+  p.sa = a->scale_inv;
+  p.sb = b->scale_inv;
+  p.C = c;
+  p.out = out;
+  p.Cq = nullptr;
+  p.q_scale = nullptr;
+  p.q_fmt = 0;
+  p.amax = nullptr;
+  p.ws = nullptr;
+  p.part = nullptr;
+  p.M = depth ? n : rows;
+  p.N = depth ? k : n;
+  p.K = kc;
+  p.fa = a->fmt;
+  p.fb = b->fmt;
+  p.mode = mode;
+  p.bra = 1;
+  p.brb = b->scaling == FP8_SCALE_BLOCK_128x128 ? 128 : 1;
+  p.offsets = offsets;
+  p.experts = experts;
+  return hip(fp8sg::launch_gemm_grouped(p, depth, st(stream)));
 }
 
 // amax / per-tensor cast of BF16 (in = 0) or FP32 (in = 1) input.
@@ -466,6 +526,32 @@ fp8_status_t fp8_gemm_wgrad_f32(const fp8_operand_t* dyT, const fp8_operand_t* x
                                 void* stream) {
   if (accumulate != 0 && accumulate != 1) return FP8_ERR_UNSUPPORTED;
   return gemm(dyT, xT, N, K, M, dw_f32, stream, accumulate ? 2 : 1);
+}
+
+fp8_status_t fp8_gemm_grouped_fprop(const fp8_operand_t* x, const fp8_operand_t* w,
+                                    const int32_t* offsets, int32_t experts, int64_t rows,
+                                    int64_t N, int64_t K, void* y_bf16, void* stream) {
+  return grouped(x, w, offsets, experts, rows, N, K, y_bf16, false, 0, stream);
+}
+
+fp8_status_t fp8_gemm_grouped_dgrad(const fp8_operand_t* dy, const fp8_operand_t* wT,
+                                    const int32_t* offsets, int32_t experts, int64_t rows,
+                                    int64_t N, int64_t K, void* dx_bf16, void* stream) {
+  return grouped(dy, wT, offsets, experts, rows, K, N, dx_bf16, false, 0, stream);
+}
+
+fp8_status_t fp8_gemm_grouped_wgrad(const fp8_operand_t* dyT, const fp8_operand_t* xT,
+                                    const int32_t* offsets, int32_t experts, int64_t rows,
+                                    int64_t N, int64_t K, void* dw_bf16, void* stream) {
+  return grouped(dyT, xT, offsets, experts, rows, N, K, dw_bf16, true, 0, stream);
+}
+
+fp8_status_t fp8_gemm_grouped_wgrad_f32(const fp8_operand_t* dyT, const fp8_operand_t* xT,
+                                        const int32_t* offsets, int32_t experts, int64_t rows,
+                                        int64_t N, int64_t K, float* dw_f32, int32_t accumulate,
+                                        void* stream) {
+  if (accumulate != 0 && accumulate != 1) return FP8_ERR_UNSUPPORTED;
+  return grouped(dyT, xT, offsets, experts, rows, N, K, dw_f32, true, accumulate ? 2 : 1, stream);
 }
 
 fp8_status_t fp8_convert_f32(const float* x, int64_t n, int32_t fmt, uint8_t* q, void* stream) {

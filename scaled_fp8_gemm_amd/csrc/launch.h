@@ -281,4 +281,25 @@ struct GemmProblem {
 hipError_t launch_gemm(const GemmProblem& p, hipStream_t s);
 hipError_t launch_gemm_mx_k32(const GemmProblem& p, hipStream_t s);
 
+// A product whose rows, or whose depth, are in segments by expert, or one with
+// 4-bit operands (MX; B's or both formats 4 = E2M1).
+//   rows:   A [M][K] in segments, B and its scales [experts][N][K], C [M][N]
+//   depth:  A [M][K], B [N][K], segments along K, C [experts][M][N]
+// offsets NULL: one segment (experts 1), all of A's rows.
+struct SegProblem : GemmProblem {
+  const int32_t* offsets = nullptr;   // device, experts + 1
+  int experts = 1;
+};
+hipError_t launch_gemm_grouped(const SegProblem& p, bool depth, hipStream_t s);
+hipError_t launch_gemm_fp4(const SegProblem& p, hipStream_t s);
+// Their kernels, by the size of an output tile: bm = 128 or 256 rows x 256
+// columns, or 16 na rows x 32 columns for few rows (na = 1, 2, 4).
+hipError_t launch_seg_tensor(const SegProblem& p, int bm, hipStream_t s);
+hipError_t launch_seg_mx(const SegProblem& p, int bm, hipStream_t s);
+hipError_t launch_seg_block(const SegProblem& p, int bm, hipStream_t s);
+hipError_t launch_seg_depth(const SegProblem& p, hipStream_t s);
+hipError_t launch_seg_fp4(const SegProblem& p, int bm, hipStream_t s);
+hipError_t launch_few(const SegProblem& p, int na, hipStream_t s);
+hipError_t launch_few_fp4(const SegProblem& p, int na, hipStream_t s);
+
 }  // namespace fp8sg

@@ -97,6 +97,10 @@ def lib():
             "fp8_gemm_wgrad": [vp, vp, i64, i64, i64, vp, vp],
             "fp8_gemm_wgrad_f32": [vp, vp, i64, i64, i64, vp, i32, vp],
             "fp8_gemm_fprop_fused": [vp, vp, i64, i64, i64, vp, i32, vp, vp, vp, vp, vp],
+            "fp8_gemm_grouped_fprop": [vp, vp, vp, i32, i64, i64, i64, vp, vp],
+            "fp8_gemm_grouped_dgrad": [vp, vp, vp, i32, i64, i64, i64, vp, vp],
+            "fp8_gemm_grouped_wgrad": [vp, vp, vp, i32, i64, i64, i64, vp, vp],
+            "fp8_gemm_grouped_wgrad_f32": [vp, vp, vp, i32, i64, i64, i64, vp, i32, vp],
             "fp8_convert_f32": [vp, i64, i32, vp, vp],
             "fp8_layernorm_fwd": [vp, i32, vp, vp, i32, i64, i64, ctypes.c_float, vp, vp, vp, vp,
                                   vp, vp, vp],
@@ -427,11 +431,11 @@ def operand(data, fmt, scaling, scale_inv) -> Operand:
     return o
 
 
-def _check_operand(o: Operand, name, rows, kc):
+def _check_operand(o: Operand, name, rows, kc, tensors=1):
     data, sc = o._tensors
-    _t(data, f"{name}.data", _U8, rows * kc)
+    _t(data, f"{name}.data", _U8, rows * kc // (2 if o.fmt == FP4_E2M1 else 1))
     if o.scaling == SCALE_TENSOR:
-        _t(sc, f"{name}.scale_inv", _F32, 1 if rows * kc else 0)
+        _t(sc, f"{name}.scale_inv", _F32, tensors if rows * kc else 0)
     elif o.scaling == SCALE_BLOCK_1x128:
         _t(sc, f"{name}.scale_inv", _F32, rows * _blocks(kc, 128))
     elif o.scaling == SCALE_BLOCK_128x128:
@@ -485,6 +489,52 @@ def fp8_gemm_wgrad_f32(dyT: Operand, xT: Operand, M, N, K, dw, accumulate=False,
                                     1 if accumulate else 0, _stream(stream)))
 
 
+def _grouped(x, w, offsets, experts, rows, n, k, y, names):
+    """y[rows][n] = x[rows][k] in segments times w[experts][n][k]: the checked
+    pointers of x, w, offsets and y."""
+    return (_held(x, names[0], rows, k), _held(w, names[1], experts * n, k, experts),
+            _t(offsets, "offsets", _I32, experts + 1), _t(y, names[2], _BF16, rows * n))
+
+
+def fp8_gemm_grouped_fprop(x: Operand, w: Operand, offsets, experts, rows, N, K, y, stream=None):
+    """y[r] = x[r] w[e]^T for the rows r of every expert's segment
+    [offsets[e], offsets[e + 1]): x [rows][K], w [experts][N][K], y [rows][N]
+    BF16; rows in no segment are left alone."""
+    xp, wp, op, yp = _grouped(x, w, offsets, experts, rows, N, K, y, ("x", "w", "y"))
+    _check("fp8_gemm_grouped_fprop",
+           lib().fp8_gemm_grouped_fprop(xp, wp, op, experts, rows, N, K, yp, _stream(stream)))
+
+
+def fp8_gemm_grouped_dgrad(dy: Operand, wT: Operand, offsets, experts, rows, N, K, dx,
+                           stream=None):
+    """dx[r] = dy[r] wT[e]^T: dy [rows][N], wT [experts][K][N], dx [rows][K]."""
+    dp, wp, op, xp = _grouped(dy, wT, offsets, experts, rows, K, N, dx, ("dy", "wT", "dx"))
+    _check("fp8_gemm_grouped_dgrad",
+           lib().fp8_gemm_grouped_dgrad(dp, wp, op, experts, rows, N, K, xp, _stream(stream)))
+
+
+def _grouped_wgrad(dyT, xT, offsets, experts, rows, N, K, dw, dtypes):
+    return (_held(dyT, "dyT", N, rows), _held(xT, "xT", K, rows),
+            _t(offsets, "offsets", _I32, experts + 1), experts, rows, N, K,
+            _t(dw, "dw", dtypes, experts * N * K))
+
+
+def fp8_gemm_grouped_wgrad(dyT: Operand, xT: Operand, offsets, experts, rows, N, K, dw,
+                           stream=None):
+    """dw[e] = the product of dyT [N][rows] and xT [K][rows] over segment e's
+    rows: dw [experts][N][K] BF16, zeros for an expert without rows."""
+    _check("fp8_gemm_grouped_wgrad", lib().fp8_gemm_grouped_wgrad(
+        *_grouped_wgrad(dyT, xT, offsets, experts, rows, N, K, dw, _BF16), _stream(stream)))
+
+
+def fp8_gemm_grouped_wgrad_f32(dyT: Operand, xT: Operand, offsets, experts, rows, N, K, dw,
+                               accumulate=False, stream=None):
+    """The same in FP32, added to dw with `accumulate`."""
+    _check("fp8_gemm_grouped_wgrad_f32", lib().fp8_gemm_grouped_wgrad_f32(
+        *_grouped_wgrad(dyT, xT, offsets, experts, rows, N, K, dw, _F32), 1 if accumulate else 0,
+        _stream(stream)))
+
+
 # ------------------------------------------------------------ row operators
 def cast_out(data, fmt, scaling, scale_inv=None, scale=None, amax=None) -> CastOut:
     """An FP8 output of a row operator: `scale_inv` receives the scales of
@@ -521,11 +571,12 @@ def _wants_amax(o):
     return isinstance(o, CastOut) and o.scaling == SCALE_TENSOR and o.amax is not None
 
 
-def _held(o: Operand, name, rows, cols):
-    """Checks a checkpoint of [rows][cols] that a call reads."""
+def _held(o: Operand, name, rows, cols, tensors=1):
+    """Checks an operand of [rows][cols] that a call reads, of so many tensors
+    with a scale each."""
     if not isinstance(o, Operand):
         raise TypeError(f"{name} must be an operand()")
-    _check_operand(o, name, rows, cols)
+    _check_operand(o, name, rows, cols, tensors)
     return ctypes.byref(o)
 
 

@@ -75,7 +75,7 @@ def pack(code):
 
 
 def unpack(q):
-    return torch.stack([q.long() % 16, q.long() // 16], -1).view(q.shape[0], -1)
+    return torch.stack([q.long() % 16, q.long() // 16], -1).view(q.shape[0], 2 * q.shape[1])
 
 
 def mx4_values(q, byte):
