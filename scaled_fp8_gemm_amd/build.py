@@ -17,7 +17,7 @@ LIB = os.path.join(PKG, "libfp8sg.so")
 SOURCES = ["abi.hip", "quant.hip", "gemm.hip", "gemm_mx_k32.hip",
            "layernorm.hip", "act.hip", "moe.hip", "rmsnorm.hip", "quant4.hip",
            "gemm_grouped.hip", "gemm_seg_tensor.hip", "gemm_seg_mx.hip", "gemm_seg_block.hip",
-           "gemm_seg_depth.hip", "gemm_few.hip", "gemm_fp4.hip"]
+           "gemm_seg_depth.hip", "gemm_fp4.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

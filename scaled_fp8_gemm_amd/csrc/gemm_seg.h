@@ -7,16 +7,16 @@
 // Segment e is [offsets[e], offsets[e + 1]), read on the device; without
 // offsets there is one segment, all rows.
 //
-// Design, as gemm.hip: 8 waves a workgroup, an output tile of BM x 256, the
-// operands' tiles of one step straight from memory into one of two LDS stages
-// (buffer_load ... lds) while the MFMAs work on the other, scales of 512 K by
-// the same way.  A step is 128 bytes of a row: 128 K, or 256 K where both
-// operands have 4 bits, whose v_mfma takes half the time; a 4-bit operand
-// beside an 8-bit one has rows of 64 bytes a step.  What is different:
+// Design, as gemm.hip: an output tile a workgroup, the operands' tiles of one
+// step straight from memory into one of the LDS stages (buffer_load ... lds)
+// while the MFMAs work on another, scales of 512 K by the same way.  A step is
+// 128 bytes of a row: 128 K, or 256 K where both operands have 4 bits, whose
+// v_mfma takes half the time; a 4-bit operand beside an 8-bit one has rows of
+// 64 bytes a step.  What is different:
 //   * a workgroup finds its expert itself: every wave scans the segments'
 //     tile counts, 64 experts at a time, so the host need not know them;
 //   * loads and stores end with the segment, not with the matrix;
-//   * BM = 128 (waves 2 x 4 instead of 4 x 2) where segments are short;
+//   * smaller tiles where segments are short;
 //   * depth: a row's stride and the length of its segment are two numbers.
 #pragma once
 
@@ -30,7 +30,6 @@ namespace {
 namespace seg {
 
 constexpr int kE2M1 = 4;
-constexpr int BN = 256, NT = 512, NW = 8;
 
 struct SegArgs {
   Args g;                  // M: rows of A; C: of expert 0
@@ -65,6 +64,14 @@ __device__ __forceinline__ int lane_value(int v, int lane) {
 struct Place {
   int e, from, to, count, local;
 };
+template <int BM>
+__device__ __forceinline__ int tile_rows(const SegArgs& p) {
+  if (p.offsets == nullptr) return p.g.tiles_m;
+  int total = 0, from, to;
+  for (int c = 0; c < p.experts; c += 64)
+    total += lane_value(wave_scan(tiles_of(p, c + (int)(threadIdx.x & 63), BM, from, to)), 63);
+  return total;
+}
 template <int BM, bool XCD>
 __device__ __forceinline__ bool find(const SegArgs& p, int tiles_n, int at, Place& w) {
   const int lane = threadIdx.x & 63;
@@ -130,7 +137,7 @@ __device__ __forceinline__ void walk(int t, int tiles_m, int tiles_n, int& tm, i
 // c ^ turn(r), so that the 16 rows of a fragment read fall into all banks.
 template <int RB>
 __device__ __forceinline__ int turn(int row) {
-  return RB == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
+  return RB == 256 ? row & 15 : RB == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
 }
 template <int RB>
 __device__ __forceinline__ int place(int row, int chunk) {
@@ -141,7 +148,7 @@ __device__ __forceinline__ int place(int row, int chunk) {
 // load, lane l to byte 16 l of it.  `stride`: bytes from row to row; `depth`:
 // bytes of a row that belong to the product, chunks past it read as zeros, as
 // do rows past `rows`.
-template <int ROWS, int RB>
+template <int ROWS, int RB, int NW>
 struct Loader {
   static constexpr int L = ROWS * RB / (1024 * NW);
   static constexpr int R = 1024 / RB;           // rows of a load
@@ -207,41 +214,56 @@ __device__ __forceinline__ v8i fragment(const uint8_t* __restrict__ s, int row0,
     const uint4 v = *reinterpret_cast<const uint4*>(s + place<RB>(r, 4 * h + g));
     o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
   } else {
-    const uint4 lo = *reinterpret_cast<const uint4*>(s + place<RB>(r, g));
-    const uint4 hi = *reinterpret_cast<const uint4*>(s + place<RB>(r, g + 4));
+    const uint4 lo = *reinterpret_cast<const uint4*>(s + place<RB>(r, 8 * h + g));
+    const uint4 hi = *reinterpret_cast<const uint4*>(s + place<RB>(r, 8 * h + g + 4));
     o[0] = lo.x; o[1] = lo.y; o[2] = lo.z; o[3] = lo.w;
     o[4] = hi.x; o[5] = hi.y; o[6] = hi.z; o[7] = hi.w;
   }
   return o;
 }
 
+// The output tile, its waves (each a part of the tile), the LDS stages, and the
+// bytes of a row in a step.
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, int ROW_ = 128>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
+  static constexpr int STAGES = STAGES_, ROW = ROW_, NW = WAVES_M * WAVES_N, NT = 64 * NW;
+  static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
+};
+
 // MODE: tensor, block (BRB: rows of B a scale) or MX.  DIRECT (MX rows of a
 // length that is no multiple of 128, whose scale bytes are not aligned
 // dwords): every lane loads its scale bytes from memory, one step ahead.
-template <int MODE, int FA, int FB, int BRB, int BM, bool DEPTH, bool DIRECT>
-__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2, 2)))
+template <int MODE, int FA, int FB, int BRB, class T, bool DEPTH, bool DIRECT>
+__global__ __launch_bounds__(T::NT) __attribute__((amdgpu_waves_per_eu(2)))
 void k_gemm_seg(SegArgs p) {
-  static_assert(BM == 256 || BM == 128, "tile rows");
   static_assert(!DIRECT || (MODE == kMX && !DEPTH), "scale bytes from memory");
+  constexpr int BM = T::BM, BN = T::BN, NW = T::NW, NT = T::NT, STAGES = T::STAGES;
   constexpr bool STAGED = MODE != kTensor && !DIRECT;
-  constexpr int KS = FA == kE2M1 && FB == kE2M1 ? 256 : 128, SUB = KS / 128;
+  constexpr int KS = FA == kE2M1 && FB == kE2M1 ? 2 * T::ROW : T::ROW, SUB = KS / 128;
   constexpr int RA = FA == kE2M1 ? KS / 2 : KS, RB = FB == kE2M1 ? KS / 2 : KS;
-  constexpr int WAVES_M = BM / 64, WN = BN * WAVES_M / NW;
-  constexpr int NF = 4, NJ = WN / 16;
+  constexpr int WM = T::WM, WN = T::WN, NF = WM / 16, NJ = WN / 16;
   constexpr int A_BYTES = BM * RA, B_BYTES = BN * RB, STAGE = A_BYTES + B_BYTES;
-  static_assert(2 * STAGE >= 128 * 512, "half an output tile is staged in LDS");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][STAGE];
-  __shared__ __attribute__((aligned(16))) uint32_t lS[STAGED ? 2 : 1][STAGED ? (BM + BN) * 4 : 4];
-  __shared__ uint32_t red[NT / 64];
+  constexpr int CHUNK = 512 / KS;              // steps of 512 K of scales
+  // columns that a B fragment is read before its products
+  constexpr int AHEAD = 1;
+  // chunks that the steps in flight and the present one can be of
+  constexpr int CHUNKS = (STAGES - 2 + CHUNK) / CHUNK + 1;
+  // scale rows, A's first, 64 a wave's load
+  constexpr int AS = (BM + 63) / 64, BS = (BN + 63) / 64, SW = AS + BS;
+  static_assert(SW <= NW, "64 rows of scales a wave");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES][STAGE];
+  __shared__ __attribute__((aligned(16))) uint32_t lS[STAGED ? CHUNKS : 1][STAGED ? SW * 256 : 4];
+  __shared__ uint32_t red[NW];
   Place at;
   int tm, tn;
   if constexpr (DEPTH) {
     // every expert's tiles spread over the XCDs by themselves: the experts'
     // depths differ
-    const int T = p.g.tiles_m * p.g.tiles_n, grid = (T + 7) / 8 * 8;
+    const int tiles = p.g.tiles_m * p.g.tiles_n, grid = (tiles + 7) / 8 * 8;
     at.e = blockIdx.x / grid;
     const int b = blockIdx.x - at.e * grid, t = (b & 7) * (grid / 8) + (b >> 3);
-    if (t >= T) return;
+    if (t >= tiles) return;
     walk(t, p.g.tiles_m, p.g.tiles_n, tm, tn);
     const int rows = (int)p.g.K;             // A's and B's row length: all segments
     constexpr int unit = MODE == kTensor ? 16 : 128;
@@ -257,7 +279,7 @@ void k_gemm_seg(SegArgs p) {
   const int64_t m_end = DEPTH ? p.g.M : at.to;
   const int64_t depth = DEPTH ? at.to - at.from : p.g.K;       // K of the product
   const int lane = threadIdx.x & 63, w = wave_id();
-  const int wm = w % WAVES_M, wn = w / WAVES_M;
+  const int wm = w / T::WAVES_N, wn = w % T::WAVES_N;
   const int g = lane >> 4, lr = lane & 15;
   const int nk = (int)((depth + KS - 1) / KS);
   Args out = p.g;
@@ -274,8 +296,8 @@ void k_gemm_seg(SegArgs p) {
 
   constexpr int DA = FA == kE2M1 ? 2 : 1, DB = FB == kE2M1 ? 2 : 1;   // elements a byte
   const int64_t lda = p.g.K / DA, ldb = p.g.K / DB;
-  Loader<BM, RA> la;
-  Loader<BN, RB> lb;
+  Loader<BM, RA, NW> la;
+  Loader<BN, RB, NW> lb;
   la.init(p.g.A + m0 * lda + (DEPTH ? at.from / DA : 0), m_end - m0, lda, depth / DA, w);
   lb.init(p.g.B + (DEPTH ? n0 * ldb + at.from / DB : (at.e * p.g.N + n0) * ldb), p.g.N - n0, ldb,
           depth / DB, w);
@@ -291,19 +313,25 @@ void k_gemm_seg(SegArgs p) {
     sb += (DEPTH ? n0 : (at.e * p.g.N + n0) / BRB) * row_bytes + skip;
     if constexpr (STAGED) {
       const int64_t bytes = (depth + PER - 1) / PER * SB;
-      if (w < BM / 64)
+      if (w < AS)
         ls.init(sa, (int)min(m_end - m0, (int64_t)BM), 1, row_bytes, bytes, w);
       else
-        ls.init(sb, (int)min(p.g.N - n0, (int64_t)BN), BRB, row_bytes, bytes, w - BM / 64);
+        ls.init(sb, (int)min(p.g.N - n0, (int64_t)BN), BRB, row_bytes, bytes, w - AS);
     }
   }
-  constexpr int CHUNK = 512 / KS;                              // steps of 512 K
-  auto issue = [&](int stage, int kt) {
-    la.load(lds[stage], kt);
-    lb.load(lds[stage] + A_BYTES, kt);
-    if constexpr (STAGED)
-      if (kt % CHUNK == 0 && w < (BM + BN) / 64)
-        ls.load(lds_addr(&lS[(kt / CHUNK) & 1][w * 256]), kt / CHUNK);
+  // The loads of step kt, as many in every step where more than one is in
+  // flight (a step past the end reads nothing); scales come in addition, which
+  // makes the wait for a step a little longer than it need be.
+  constexpr int LOADS = Loader<BM, RA, NW>::L + Loader<BN, RB, NW>::L;
+  int into = 0;                                // the stage of the next step to load
+  auto issue = [&](int kt) {
+    if constexpr (STAGED) {
+      if (kt % CHUNK == 0 && w < SW)
+        ls.load(lds_addr(&lS[(kt / CHUNK) % CHUNKS][w * 256]), kt / CHUNK);
+    }
+    la.load(lds[into], kt);
+    lb.load(lds[into] + A_BYTES, kt);
+    into = into + 1 == STAGES ? 0 : into + 1;
   };
   // DIRECT: this lane's scale bytes of step kt, 1 where there is no block
   struct Bytes {
@@ -317,7 +345,7 @@ void k_gemm_seg(SegArgs p) {
       const bool in = blk < row;
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
-        const int r = wm * 64 + f * 16 + lr;
+        const int r = wm * WM + f * 16 + lr;
         s.a[h][f] = in && m0 + r < m_end ? sa[r * row + blk] : 127;
       }
 #pragma unroll
@@ -330,96 +358,133 @@ void k_gemm_seg(SegArgs p) {
   Bytes now, next;
 
   if (nk > 0) {
-    issue(0, 0);
     if constexpr (DIRECT) fetch(now, 0);
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i)
+      if (STAGES > 2 || i < nk) issue(i);
   }
-  wait_vm<0>();
-  __syncthreads();
 
+  // a wave whose part of the tile is outside the segment or the columns moves
+  // data only (waves share their SIMD with one of other rows)
+  const bool idle = m0 + wm * WM >= m_end || n0 + wn * WN >= p.g.N;
+  int cur = 0;
   for (int kt = 0; kt < nk; ++kt) {
-    const int cur = kt & 1;
+    // step kt has landed, for every wave, and the stage before it is free
+    wait_vm<LOADS * (STAGES - 2)>();
+    __syncthreads();
     const uint8_t* As = lds[cur];
     const uint8_t* Bs = lds[cur] + A_BYTES;
-    const uint32_t* S = lS[STAGED ? (kt / CHUNK) & 1 : 0];
+    cur = cur + 1 == STAGES ? 0 : cur + 1;
+    const uint32_t* S = lS[STAGED ? (kt / CHUNK) % CHUNKS : 0];
     const uint8_t* S8 = reinterpret_cast<const uint8_t*>(S);
     const float* Sf = reinterpret_cast<const float*>(S);
+    const int brow = AS * 64 + wn * WN;         // scale row of this wave's first column
+    // The step's columns of fragments, c = h NJ + j: column c's B fragment is
+    // read AHEAD columns before its products, the A fragments of sub-step h
+    // among the columns of the sub-step before.
+    v8i af[SUB > 1 ? 2 : 1][NF], bf[AHEAD + 1];
+    int ea[SUB > 1 ? 2 : 1][NF], eb[AHEAD + 1];
+    float sa_f[NF];
+    const auto read_a = [&](int h, int f) {
+      af[h & (SUB > 1)][f] = fragment<FA, RA>(As, wm * WM + f * 16, h);
+      if constexpr (MODE == kMX && STAGED)
+        ea[h & (SUB > 1)][f] = S8[((wm * WM + f * 16 + lr) * 4 + (kt % CHUNK) * SUB + h) * 4 + g];
+    };
+    const auto read_b = [&](int c) {
+      const int h = c / NJ, j = c % NJ;
+      bf[c % (AHEAD + 1)] = fragment<FB, RB>(Bs, wn * WN + j * 16, h);
+      if constexpr (MODE == kMX && STAGED)
+        eb[c % (AHEAD + 1)] = S8[((brow + j * 16 + lr) * 4 + (kt % CHUNK) * SUB + h) * 4 + g];
+    };
+    if (!idle) {
 #pragma unroll
-    for (int h = 0; h < SUB; ++h) {
-      // past the end of K the data are zeros, but the scale bytes may be NaN
-      if (SUB > 1 && h > 0 && (int64_t)kt * KS + h * 128 >= depth) break;
-      const int sw = (kt % CHUNK) * SUB + h;
-      v8i af[NF], bf[2];
+      for (int f = 0; f < NF; ++f) read_a(0, f);
 #pragma unroll
-      for (int f = 0; f < NF; ++f) af[f] = fragment<FA, RA>(As, wm * 64 + f * 16, h);
-      bf[0] = fragment<FB, RB>(Bs, wn * WN, h);
-      float sa_f[NF];
-      int ea[NF], eb[2];
-      const int brow = BM + wn * WN;          // scale row of this wave's first column
+      for (int c = 0; c < AHEAD; ++c)
+        if (c < SUB * NJ) read_b(c);
+    }
+    if (kt + STAGES - 1 < nk || STAGES > 2) issue(kt + STAGES - 1);
+    if constexpr (DIRECT)
+      if (kt + 1 < nk) fetch(next, kt + 1);
+    if (idle) continue;
+    v4f P[2][NF];
+    const auto scales_of = [&](int h) {         // block mode: A's, times B's where it is one
       if constexpr (MODE == kBlock) {
+        const int sw = (kt % CHUNK) * SUB + h;
 #pragma unroll
-        for (int f = 0; f < NF; ++f) sa_f[f] = Sf[(wm * 64 + f * 16 + lr) * 4 + sw];
+        for (int f = 0; f < NF; ++f) sa_f[f] = Sf[(wm * WM + f * 16 + lr) * 4 + sw];
         if constexpr (BRB == 128) {
           const float sb_u = Sf[brow * 4 + sw];
 #pragma unroll
           for (int f = 0; f < NF; ++f) sa_f[f] *= sb_u;
         }
-      } else if constexpr (MODE == kMX && STAGED) {
-#pragma unroll
-        for (int f = 0; f < NF; ++f) ea[f] = S8[((wm * 64 + f * 16 + lr) * 4 + sw) * 4 + g];
-        eb[0] = S8[((brow + lr) * 4 + sw) * 4 + g];
       }
-      if (h == 0 && kt + 1 < nk) {
-        issue(cur ^ 1, kt + 1);
-        if constexpr (DIRECT) fetch(next, kt + 1);
+    };
+    const auto promote = [&](int c) {           // acc += scales * P of column c
+      if constexpr (MODE == kBlock) {
+        const int h = c / NJ, j = c % NJ, sw = (kt % CHUNK) * SUB + h;
+        float b[4] = {1.f, 1.f, 1.f, 1.f};
+        if constexpr (BRB == 1) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) b[r] = Sf[(brow + j * 16 + 4 * g + r) * 4 + sw];
+        }
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[f][j][r] += (BRB == 1 ? sa_f[f] * b[r] : sa_f[f]) * P[c & 1][f][r];
+      }
+    };
+    scales_of(0);
+    bool ended = false;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int c = 0; c < SUB * NJ; ++c) {
+      const int h = c / NJ, j = c % NJ;
+      // past the end of K the data are zeros, but the scale bytes may be NaN
+      if (h > 0 && j == 0 && (int64_t)kt * KS + h * 128 >= depth) {
+        if constexpr (MODE == kBlock) promote(c - 1);
+        ended = true;
+        break;
+      }
+      if (c + AHEAD < SUB * NJ) read_b(c + AHEAD);
+      if (h + 1 < SUB) {
+        if constexpr (NJ > NF) {
+          if (j >= NJ - 1 - NF && j < NJ - 1) read_a(h + 1, j - (NJ - 1 - NF));
+        } else {
+          if (j == 0)
+#pragma unroll
+            for (int f = 0; f < NF; ++f) read_a(h + 1, f);
+        }
+      }
+      const v8i b = bf[c % (AHEAD + 1)];
+      const v8i(&a)[NF] = af[h & (SUB > 1)];
+      if constexpr (MODE == kTensor) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f) acc[f][j] = mfma<FB, FA>(b, a[f], acc[f][j]);
+      } else if constexpr (MODE == kMX) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+          acc[f][j] = mfma_mx<FB, FA>(b, a[f], acc[f][j],
+                                      STAGED ? eb[c % (AHEAD + 1)] : now.b[h][j],
+                                      STAGED ? ea[h & (SUB > 1)][f] : now.a[h][f]);
+      } else {
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+          P[c & 1][f] = mfma<FB, FA>(b, a[f], v4f{0.f, 0.f, 0.f, 0.f});
+        // column c's MFMAs stay ahead of column c - 1's scaling
+        __builtin_amdgcn_sched_barrier(0);
+        if (c > 0) promote(c - 1);
+        if (h > 0 && j == 0) scales_of(h);
       }
       __builtin_amdgcn_sched_barrier(0);
-      v4f P[2][NF];
-      const auto promote = [&](int j) {       // acc += scales * P of column j
-        if constexpr (MODE == kBlock) {
-          float b[4] = {1.f, 1.f, 1.f, 1.f};
-          if constexpr (BRB == 1) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) b[r] = Sf[(brow + j * 16 + 4 * g + r) * 4 + sw];
-          }
-#pragma unroll
-          for (int f = 0; f < NF; ++f)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              acc[f][j][r] += (BRB == 1 ? sa_f[f] * b[r] : sa_f[f]) * P[j & 1][f][r];
-        }
-      };
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        if (j + 1 < NJ) {
-          bf[(j + 1) & 1] = fragment<FB, RB>(Bs, wn * WN + (j + 1) * 16, h);
-          if constexpr (MODE == kMX && STAGED)
-            eb[(j + 1) & 1] = S8[((brow + (j + 1) * 16 + lr) * 4 + sw) * 4 + g];
-        }
-        if constexpr (MODE == kTensor) {
-#pragma unroll
-          for (int f = 0; f < NF; ++f) acc[f][j] = mfma<FB, FA>(bf[j & 1], af[f], acc[f][j]);
-        } else if constexpr (MODE == kMX) {
-#pragma unroll
-          for (int f = 0; f < NF; ++f)
-            acc[f][j] = mfma_mx<FB, FA>(bf[j & 1], af[f], acc[f][j],
-                                        STAGED ? eb[j & 1] : now.b[h][j],
-                                        STAGED ? ea[f] : now.a[h][f]);
-        } else {
-#pragma unroll
-          for (int f = 0; f < NF; ++f)
-            P[j & 1][f] = mfma<FB, FA>(bf[j & 1], af[f], v4f{0.f, 0.f, 0.f, 0.f});
-          // column j's MFMAs stay ahead of column j - 1's scaling
-          __builtin_amdgcn_sched_barrier(0);
-          if (j > 0) promote(j - 1);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if constexpr (MODE == kBlock) promote(NJ - 1);
     }
+    if constexpr (MODE == kBlock)
+      if (!ended) promote(SUB * NJ - 1);
     if constexpr (DIRECT) now = next;
-    wait_vm<0>();
-    __syncthreads();
   }
+  wait_vm<0>();
+  __syncthreads();
 
   // Epilogue, as gemm.hip's.
   const float qs = out.Cq != nullptr ? *out.q_scale : 1.0f;
@@ -428,40 +493,41 @@ void k_gemm_seg(SegArgs p) {
   if constexpr (MODE == kTensor)
     s = static_cast<const float*>(p.g.sa)[0] * static_cast<const float*>(p.g.sb)[DEPTH ? 0 : at.e];
   if (out.out == 0 && out.Cq == nullptr && out.part == nullptr && (out.N & 7) == 0) {
-    // 128 rows of 512 bytes at a time through LDS, 16-byte chunks XOR-swizzled
-    // by row, so that global stores cover whole rows
+    // up to 128 rows at a time through LDS, 16-byte chunks XOR-swizzled by
+    // row, so that global stores cover whole rows
+    constexpr int PART = BM < 128 ? BM : 128, CH = BN / 8, ROW = BN * 2, PASS = NT / CH;
+    static_assert(PART * ROW <= STAGES * STAGE, "the staged rows");
     uint8_t* stage = &lds[0][0];
 #pragma unroll
-    for (int part = 0; part < BM / 128; ++part) {
+    for (int part = 0; part < BM / PART; ++part) {
       if (part > 0) __syncthreads();
-      if (wm / 2 == part) {
+      if (wm * WM / PART == part) {
 #pragma unroll
         for (int f = 0; f < NF; ++f)
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
             const v4f a = acc[f][j];
-            const int r = (wm & 1) * 64 + f * 16 + lr, c = wn * WN + j * 16 + 4 * g;
-            *reinterpret_cast<uint2*>(stage + r * 512 + (((c >> 3) ^ (r & 31)) << 4) +
+            const int r = (wm * WM) % PART + f * 16 + lr, c = wn * WN + j * 16 + 4 * g;
+            *reinterpret_cast<uint2*>(stage + r * ROW + (((c >> 3) ^ (r & (CH - 1))) << 4) +
                                       ((c >> 2) & 1) * 8) =
                 make_uint2(pack_bf16x2(a[0] * s, a[1] * s), pack_bf16x2(a[2] * s, a[3] * s));
           }
       }
       __syncthreads();
-      const int t = threadIdx.x, ch = t & 31;
+      const int t = threadIdx.x, ch = t % CH;
 #pragma unroll 4
-      for (int k = 0; k < 8; ++k) {
-        const int r = k * 16 + (t >> 5);
-        const int64_t m = m0 + part * 128 + r, n = n0 + ch * 8;
+      for (int r = t / CH; r < PART; r += PASS) {
+        const int64_t m = m0 + part * PART + r, n = n0 + ch * 8;
         if (m < m_end && n < out.N)
           *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out.C) + m * out.N + n) =
-              *reinterpret_cast<const uint4*>(stage + r * 512 + ((ch ^ (r & 31)) << 4));
+              *reinterpret_cast<const uint4*>(stage + r * ROW + ((ch ^ (r & (CH - 1))) << 4));
       }
     }
     return;
   }
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
-    const int64_t m = m0 + wm * 64 + f * 16 + lr;
+    const int64_t m = m0 + wm * WM + f * 16 + lr;
     if (m >= m_end) continue;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
@@ -474,36 +540,52 @@ void k_gemm_seg(SegArgs p) {
   tile_amax<NT>(out, tm, tn, mx, red);
 }
 
-// Workgroups for tiles of bm x bn; with offsets at most one tile row more an
-// expert than the rows alone would need.  A multiple of 8, so that every XCD
-// gets the same count.
-inline int64_t tiles_at_most(const SegProblem& q, int bm, int bn, bool depth) {
-  const int64_t tn = (q.N + bn - 1) / bn, tm = (q.M + bm - 1) / bm;
-  if (depth) return (tm * tn + 7) / 8 * 8 * q.experts;
-  const int64_t more = q.offsets ? (q.M < q.experts ? q.M : q.experts) : 0;
-  return ((q.offsets ? q.M / bm + more : tm) * tn + 7) / 8 * 8;
-}
+// The tiles by TileKind.  Large ones read their operands as few times as LDS
+// allows.  The smaller ones are for short segments, where loading is all:
+// several workgroups a CU, two or three steps on their way beside the one at
+// work.  That of 16 rows has steps of 256 bytes a row, twice the bytes to a
+// barrier.
+typedef Tile<256, 256, 4, 2, 2> T256;
+typedef Tile<128, 128, 2, 2, 2> T128;
+typedef Tile<64, 128, 2, 2, 3> T64x128;
+typedef Tile<64, 64, 2, 2, 3> T64;
+typedef Tile<32, 64, 1, 4, 4> T32;
+typedef Tile<16, 64, 1, 4, 3, 256> T16;
 
-inline SegArgs seg_args(const SegProblem& q, int bm) {
+inline SegArgs seg_args(const SegProblem& q, int bm, int bn) {
   SegArgs a;
   a.g.A = q.A; a.g.B = q.B; a.g.sa = q.sa; a.g.sb = q.sb; a.g.C = q.C; a.g.out = q.out;
   a.g.Cq = q.Cq; a.g.q_scale = q.q_scale; a.g.q_fmt = q.q_fmt; a.g.part = q.part;
   a.g.M = q.M; a.g.N = q.N; a.g.K = q.K;
   a.g.tiles_m = (int)((q.M + bm - 1) / bm);
-  a.g.tiles_n = (int)((q.N + BN - 1) / BN);
+  a.g.tiles_n = (int)((q.N + bn - 1) / bn);
   a.offsets = q.offsets;
   a.experts = q.experts;
   return a;
 }
 
-template <int MODE, int FA, int FB, int BRB, int BM, bool DEPTH, bool DIRECT>
+template <int MODE, int FA, int FB, int BRB, class T, bool DEPTH, bool DIRECT>
 hipError_t run(const SegProblem& q, hipStream_t s) {
-  const SegArgs a = seg_args(q, BM);
-  const int64_t T = tiles_at_most(q, BM, BN, DEPTH);
-  if (T > kMaxGrid) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((k_gemm_seg<MODE, FA, FB, BRB, BM, DEPTH, DIRECT>), dim3((unsigned)T),
-                     dim3(NT), 0, s, a);
+  const SegArgs a = seg_args(q, T::BM, T::BN);
+  const int64_t n = DEPTH ? ((int64_t)a.g.tiles_m * a.g.tiles_n + 7) / 8 * 8 * q.experts
+                          : (row_tiles(q, T::BM, T::BN) + 7) / 8 * 8;   // every XCD the same count
+  if (n > kMaxGrid) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((k_gemm_seg<MODE, FA, FB, BRB, T, DEPTH, DIRECT>), dim3((unsigned)n),
+                     dim3(T::NT), 0, s, a);
   return hipGetLastError();
+}
+template <int MODE, int FA, int FB, int BRB, bool DIRECT>
+hipError_t run_rows(const SegProblem& q, TileKind t, hipStream_t s) {
+  switch (t) {
+    case kTile256: return run<MODE, FA, FB, BRB, T256, false, DIRECT>(q, s);
+    case kTile128: return run<MODE, FA, FB, BRB, T128, false, DIRECT>(q, s);
+    case kTile64x128: return run<MODE, FA, FB, BRB, T64x128, false, DIRECT>(q, s);
+    case kTile64: return run<MODE, FA, FB, BRB, T64, false, DIRECT>(q, s);
+    case kTile32: return run<MODE, FA, FB, BRB, T32, false, DIRECT>(q, s);
+    case kTile16: break;
+  }
+  if constexpr (FB == kE2M1) return run<MODE, FA, FB, BRB, T16, false, DIRECT>(q, s);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace seg

@@ -6,19 +6,18 @@ namespace fp8sg {
 
 namespace {
 
-template <int BRB, int BM>
-hipError_t run_block(const SegProblem& q, hipStream_t s) {
-  if (q.fa == kE4M3 && q.fb == kE4M3) return seg::run<kBlock, kE4M3, kE4M3, BRB, BM, false, false>(q, s);
-  if (q.fa == kE5M2 && q.fb == kE4M3) return seg::run<kBlock, kE5M2, kE4M3, BRB, BM, false, false>(q, s);
-  if (q.fa == kE4M3 && q.fb == kE5M2) return seg::run<kBlock, kE4M3, kE5M2, BRB, BM, false, false>(q, s);
-  return seg::run<kBlock, kE5M2, kE5M2, BRB, BM, false, false>(q, s);
+template <int BRB>
+hipError_t run_block(const SegProblem& q, TileKind t, hipStream_t s) {
+  if (q.fa == kE4M3 && q.fb == kE4M3) return seg::run_rows<kBlock, kE4M3, kE4M3, BRB, false>(q, t, s);
+  if (q.fa == kE5M2 && q.fb == kE4M3) return seg::run_rows<kBlock, kE5M2, kE4M3, BRB, false>(q, t, s);
+  if (q.fa == kE4M3 && q.fb == kE5M2) return seg::run_rows<kBlock, kE4M3, kE5M2, BRB, false>(q, t, s);
+  return seg::run_rows<kBlock, kE5M2, kE5M2, BRB, false>(q, t, s);
 }
 
 }  // namespace
 
-hipError_t launch_seg_block(const SegProblem& q, int bm, hipStream_t s) {
-  if (q.brb == 128) return bm == 128 ? run_block<128, 128>(q, s) : run_block<128, 256>(q, s);
-  return bm == 128 ? run_block<1, 128>(q, s) : run_block<1, 256>(q, s);
+hipError_t launch_seg_block(const SegProblem& q, TileKind t, hipStream_t s) {
+  return q.brb == 128 ? run_block<128>(q, t, s) : run_block<1>(q, t, s);
 }
 
 }  // namespace fp8sg

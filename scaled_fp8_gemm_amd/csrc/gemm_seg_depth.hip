@@ -8,10 +8,10 @@ namespace {
 
 template <int MODE>
 hipError_t run_depth(const SegProblem& q, hipStream_t s) {
-  if (q.fa == kE4M3 && q.fb == kE4M3) return seg::run<MODE, kE4M3, kE4M3, 1, 256, true, false>(q, s);
-  if (q.fa == kE5M2 && q.fb == kE4M3) return seg::run<MODE, kE5M2, kE4M3, 1, 256, true, false>(q, s);
-  if (q.fa == kE4M3 && q.fb == kE5M2) return seg::run<MODE, kE4M3, kE5M2, 1, 256, true, false>(q, s);
-  return seg::run<MODE, kE5M2, kE5M2, 1, 256, true, false>(q, s);
+  if (q.fa == kE4M3 && q.fb == kE4M3) return seg::run<MODE, kE4M3, kE4M3, 1, seg::T256, true, false>(q, s);
+  if (q.fa == kE5M2 && q.fb == kE4M3) return seg::run<MODE, kE5M2, kE4M3, 1, seg::T256, true, false>(q, s);
+  if (q.fa == kE4M3 && q.fb == kE5M2) return seg::run<MODE, kE4M3, kE5M2, 1, seg::T256, true, false>(q, s);
+  return seg::run<MODE, kE5M2, kE5M2, 1, seg::T256, true, false>(q, s);
 }
 
 }  // namespace

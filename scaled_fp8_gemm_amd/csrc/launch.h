@@ -290,16 +290,26 @@ struct SegProblem : GemmProblem {
   const int32_t* offsets = nullptr;   // device, experts + 1
   int experts = 1;
 };
+// The most tiles of bm x bn that the rows can have: with offsets at most one
+// tile row more a segment than the rows alone would need.
+inline int64_t row_tiles(const SegProblem& q, int bm, int bn) {
+  const int64_t tn = (q.N + bn - 1) / bn;
+  if (!q.offsets) return (q.M + bm - 1) / bm * tn;
+  return (q.M / bm + (q.M < q.experts ? q.M : q.experts)) * tn;
+}
+// E8M0 bytes that are not aligned dwords of four blocks.
+inline bool unaligned(const SegProblem& q) {
+  return q.K % 128 != 0 || (((uintptr_t)q.sa | (uintptr_t)q.sb) & 3) != 0;
+}
 hipError_t launch_gemm_grouped(const SegProblem& p, bool depth, hipStream_t s);
 hipError_t launch_gemm_fp4(const SegProblem& p, hipStream_t s);
-// Their kernels, by the size of an output tile: bm = 128 or 256 rows x 256
-// columns, or 16 na rows x 32 columns for few rows (na = 1, 2, 4).
-hipError_t launch_seg_tensor(const SegProblem& p, int bm, hipStream_t s);
-hipError_t launch_seg_mx(const SegProblem& p, int bm, hipStream_t s);
-hipError_t launch_seg_block(const SegProblem& p, int bm, hipStream_t s);
+// Their kernels, by the output tile's rows (x columns, where they differ by
+// more than the kind says: 16 and 32 rows have 64).  kTile16: 4-bit weights.
+enum TileKind { kTile16, kTile32, kTile64, kTile64x128, kTile128, kTile256 };
+hipError_t launch_seg_tensor(const SegProblem& p, TileKind t, hipStream_t s);
+hipError_t launch_seg_mx(const SegProblem& p, TileKind t, hipStream_t s);
+hipError_t launch_seg_block(const SegProblem& p, TileKind t, hipStream_t s);
+hipError_t launch_seg_fp4(const SegProblem& p, TileKind t, hipStream_t s);
 hipError_t launch_seg_depth(const SegProblem& p, hipStream_t s);
-hipError_t launch_seg_fp4(const SegProblem& p, int bm, hipStream_t s);
-hipError_t launch_few(const SegProblem& p, int na, hipStream_t s);
-hipError_t launch_few_fp4(const SegProblem& p, int na, hipStream_t s);
 
 }  // namespace fp8sg
