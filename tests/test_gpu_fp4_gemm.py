@@ -6,6 +6,7 @@ import torch
 from tests import grouped_reference as G
 from tests.gpu_helpers import DEV
 from tests.grouped_reference import E2M1, MX
+from tests.test_gpu_grouped import some_columns
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -27,8 +28,10 @@ def operands(F, m, n, k, fa, spoil=None):
 
 
 FORMATS = [0, 1, E2M1]
-# the kernels of 16, 32, 64, 128 and 256 rows, one row and more than a tile
+# one row and more than a tile's
 ROWS = [1, 16, 17, 33, 64, 65, 130, 390, 520]
+# (rows, columns) of the tiles that need many columns: 64 x 128, 128, 256
+WIDE = [(130, 6800), (300, 10900), (520, 13907)]
 
 
 @pytest.mark.parametrize("m", ROWS)
@@ -42,8 +45,19 @@ def test_sizes(F, orc, m, n, fa):
         G.check(orc, y, av, bv, f"{k}")
 
 
+@pytest.mark.parametrize("m,n", WIDE)
+@pytest.mark.parametrize("k", [32, 160, 256, 384, 640])
+@pytest.mark.parametrize("fa", FORMATS)
+def test_wide(F, orc, m, n, k, fa):
+    (a, b), av, bv = operands(F, m, n, k, fa)
+    y = torch.full((m, n), -777.0, dtype=BF, device=DEV)
+    F.fp8_gemm_fprop(a, b, m, n, k, y)
+    cols = some_columns(n)
+    G.check(orc, y[:, cols].contiguous(), av, bv[cols], "fprop")
+
+
 @pytest.mark.parametrize("k", [32, 64, 96, 128, 256, 288, 512, 544, 640, 1024, 1056, 4096, 4640])
-@pytest.mark.parametrize("m", [3, 140])
+@pytest.mark.parametrize("m", [3, 28, 140])
 @pytest.mark.parametrize("fa", FORMATS)
 def test_depths(F, orc, m, k, fa):
     (a, b), av, bv = operands(F, m, 35, k, fa)
@@ -98,21 +112,21 @@ def test_dgrad_and_wgrad(F, orc, m, n, k):
     G.check(orc, dw, av, bv, "wgrad")
 
 
-@pytest.mark.parametrize("m", [5, 40, 140, 400])
-@pytest.mark.parametrize("n", [16, 41, 272])
+@pytest.mark.parametrize("m,n", [(5, 16), (5, 41), (28, 272), (140, 41), (400, 272)] + WIDE)
 def test_f32_out(F, m, n):
+    cols = some_columns(n)
     for fa in FORMATS:
         (a, b), av, bv = operands(F, m, n, 160, fa)
         dw = torch.full((m, n), 5.0, device=DEV)
         F.fp8_gemm_wgrad_f32(a, b, 160, m, n, dw)
-        G.check_f32(dw, torch.zeros(m, n), av, bv, "stored")
+        G.check_f32(dw[:, cols], torch.zeros(m, len(cols)), av, bv[cols], "stored")
         first = dw.clone()
         F.fp8_gemm_wgrad_f32(a, b, 160, m, n, dw, accumulate=True)
         assert torch.equal(dw, first + first)
 
 
-@pytest.mark.parametrize("m", [1, 40, 140, 520])
-@pytest.mark.parametrize("n", [16, 272])
+@pytest.mark.parametrize("m,n", [(1, 16), (30, 272), (140, 272), (130, 6800), (300, 10912),
+                                 (520, 13904)])
 @pytest.mark.parametrize("y_fmt", [0, 1])
 def test_fused(F, m, n, y_fmt):
     """The fused cast and amax are those of the BF16 output."""
