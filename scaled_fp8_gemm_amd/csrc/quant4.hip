@@ -7,7 +7,9 @@
 // byte 0xFF (NaN) and codes 0.  x * 2^-e is exact but for magnitudes that
 // round to 0, and never above 6, so a code is rounded once, by the gfx950
 // converter v_cvt_scalef32_pk_fp4_bf16 (checked for every BF16 value).
-// Two codes a byte, the first in the low half.  Bound by HBM.
+// Two codes a byte, the first in the low half.  Bound by HBM: along rows
+// 11008 x 4096 18.4 us (6.2 TB/s, part of it from the last level of cache),
+// 49152 x 12288 262 us (5.8 TB/s), 32 x 4096 2.3 us; back as fast.
 #include "quant_common.h"
 #include "launch.h"
 
@@ -51,7 +53,8 @@ __device__ __forceinline__ uint32_t quad_codes8(uint4 v, uint32_t& byte) {
 
 // Along rows.  Rows are whole blocks, so the tensor is a list of blocks: a
 // lane takes 8 elements, a quad a block, every access of a wave is contiguous.
-// U pieces of a workgroup at a time, their loads together.
+// U pieces of a workgroup at a time, their loads together: 4, which keep 64
+// bytes a lane on their way, and 1 where that would leave CUs without work.
 template <int U>
 __global__ __launch_bounds__(kThreads) void k_quant_mx4(const uint4* __restrict__ x, int64_t n8,
                                                         uint32_t* __restrict__ q,
@@ -75,33 +78,56 @@ __global__ __launch_bounds__(kThreads) void k_quant_mx4(const uint4* __restrict_
   }
 }
 
-// Both ways, a 128 x 128 tile a workgroup: rows are cast from the registers
-// they are loaded into, 16 lanes a row; the tile goes through LDS (32 KB),
-// and every thread takes two neighbouring columns of a 32-row block, whose
-// pairs of rows it packs by v_perm.  Word w of a row in row block b lies at
-// w ^ 16 b, so that the four blocks that neighbouring lanes read fall into
-// different banks.
-constexpr int kTile = 128;
-__global__ __launch_bounds__(kThreads) void k_quant_mx4_t(
-    const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t tiles_c, int64_t tile,
-    uint8_t* __restrict__ q, uint8_t* __restrict__ scale, uint8_t* __restrict__ qT,
+// Both ways, a tile of ROWS x 128 a workgroup of 2 ROWS threads: rows are cast
+// from the registers they are loaded into, 16 lanes a row; the tile goes
+// through LDS, and every thread takes two neighbouring columns of a 32-row
+// block, whose pairs of rows it packs by v_perm.  Word w of a row in row block
+// b lies at w ^ TURN b, so that the blocks that neighbouring lanes read fall
+// into different banks.
+//
+// What it writes is in pieces: 64 bytes of codes and 4 of scales to a tile's
+// row, ROWS / 2 and ROWS / 32 to a column.  So tiles of 256 rows (64 KB of
+// LDS, whole 128-byte lines along columns) where there are enough to fill the
+// device, and four neighbours to an XCD, whose L2 joins their pieces:
+//   both ways, us            128 rows   256 rows   256 rows, four to an XCD
+//   49152 x 12288               481        459        377   (4.9 TB/s)
+//   8192 x 8192                46.8       45.3       44.1
+//   4096 x 4096                13.9       13.5       13.5
+//   1024 x 4096                 5.7        6.5        6.3
+//   32 x 4096                   4.8        6.0        6.3
+// A tile held in registers ahead of the one in LDS, and scale bytes put
+// together into words, changed nothing; contiguous ranges of tiles to the XCDs
+// cost 8192 x 8192 a fifth.
+constexpr int kTile = 128, kChunk = 4;
+template <int ROWS>
+__global__ __launch_bounds__(2 * ROWS) void k_quant_mx4_t(
+    const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t tiles_c, int64_t tiles,
+    int64_t tile, uint8_t* __restrict__ q, uint8_t* __restrict__ scale, uint8_t* __restrict__ qT,
     uint8_t* __restrict__ scaleT) {
-  __shared__ __attribute__((aligned(16))) uint32_t lds[kTile * kTile / 2];
-  tile += blockIdx.x;                          // of those before this launch
-  const int64_t r0 = tile / tiles_c * kTile, c0 = tile % tiles_c * kTile;
+  constexpr int BLOCKS = ROWS / 32, TURN = 64 / BLOCKS, LANES = 2 * ROWS / 16;
+  __shared__ __attribute__((aligned(16))) uint32_t lds[ROWS * kTile / 2];
+  // `tile`: of those before this launch
+  if constexpr (ROWS > kTile) {
+    const unsigned i = blockIdx.x >> 3;
+    tile += (i / kChunk * 8 + (blockIdx.x & 7)) * kChunk + i % kChunk;
+  } else {
+    tile += blockIdx.x;
+  }
+  if (tile >= tiles) return;
+  const int64_t r0 = tile / tiles_c * ROWS, c0 = tile % tiles_c * kTile;
   const int t = threadIdx.x, slot = t & 15;
-  constexpr int U = kTile * 16 / kThreads;     // rows of a thread
+  constexpr int U = ROWS / LANES;              // rows of a thread
   uint4 v[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int r = u * (kThreads / 16) + (t >> 4);
+    const int r = u * LANES + (t >> 4);
     const bool in = r0 + r < rows && c0 + slot * 8 < cols;
     v[u] = in ? ld_stream(x + (r0 + r) * cols + c0 + slot * 8) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int r = u * (kThreads / 16) + (t >> 4);
-    *reinterpret_cast<uint4*>(&lds[r * (kTile / 2) + ((slot * 4) ^ ((r >> 5) << 4))]) = v[u];
+    const int r = u * LANES + (t >> 4);
+    *reinterpret_cast<uint4*>(&lds[r * (kTile / 2) + ((slot * 4) ^ ((r >> 5) * TURN))]) = v[u];
     if (q != nullptr) {
       uint32_t byte;
       const uint32_t w = quad_codes8(v[u], byte);
@@ -113,7 +139,7 @@ __global__ __launch_bounds__(kThreads) void k_quant_mx4_t(
     }
   }
   __syncthreads();
-  const int blk = t & 3, pair = t >> 2;        // 4 row blocks of 64 column pairs
+  const int blk = t % BLOCKS, pair = t / BLOCKS;   // of 64 column pairs
   uint32_t m2 = 0;                             // both columns' largest magnitudes
   uint32_t w[32];
   const auto top2 = [](uint32_t a, uint32_t b) {
@@ -123,7 +149,7 @@ __global__ __launch_bounds__(kThreads) void k_quant_mx4_t(
   };
 #pragma unroll
   for (int r = 0; r < 32; ++r) {
-    w[r] = lds[(blk * 32 + r) * (kTile / 2) + (pair ^ (blk << 4))];
+    w[r] = lds[(blk * 32 + r) * (kTile / 2) + (pair ^ (blk * TURN))];
     m2 = top2(m2, w[r]);
   }
   const int64_t row = r0 + blk * 32;
@@ -216,15 +242,21 @@ hipError_t launch_quantize_mx4_t(const uint16_t* x, int64_t rows, int64_t cols, 
                                  uint8_t* e8m0, uint8_t* qT, uint8_t* e8m0T, hipStream_t s) {
   if (rows == 0 || cols == 0) return hipSuccess;
   const int64_t tiles_c = (cols + kTile - 1) / kTile;
-  const int64_t tiles = (rows + kTile - 1) / kTile * tiles_c;
-  for (int64_t at = 0; at < tiles; at += kMaxGrid) {
-    const int64_t n = tiles - at < kMaxGrid ? tiles - at : kMaxGrid;
-    hipLaunchKernelGGL(k_quant_mx4_t, dim3((unsigned)n), dim3(kThreads), 0, s, x, rows, cols,
-                       tiles_c, at, q, e8m0, qT, e8m0T);
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
-  }
-  return hipSuccess;
+  const auto launch = [&](auto kernel, int tall, int round) {
+    const int64_t tiles = (rows + tall - 1) / tall * tiles_c;
+    for (int64_t at = 0; at < tiles; at += kMaxGrid) {
+      const int64_t n = tiles - at < kMaxGrid ? (tiles - at + round - 1) / round * round : kMaxGrid;
+      hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(2 * tall), 0, s, x, rows, cols, tiles_c,
+                         tiles, at, q, e8m0, qT, e8m0T);
+      const hipError_t err = hipGetLastError();
+      if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+  };
+  static_assert(kMaxGrid % (8 * kChunk) == 0, "launches of whole rounds");
+  // two workgroups a CU at least
+  if ((rows + 255) / 256 * tiles_c >= 512) return launch(k_quant_mx4_t<256>, 256, 8 * kChunk);
+  return launch(k_quant_mx4_t<128>, 128, 1);
 }
 
 hipError_t launch_dequantize_mx4(const uint8_t* q, const uint8_t* e8m0, int64_t rows, int64_t cols,

@@ -14,6 +14,18 @@
 // stream, differentiates what the forward pass computed.  All sums are in
 // FP32.  A row is read once and stays in registers between its sum and its
 // outputs.
+//
+// Bound by HBM, and by the launch below about a megabyte.  Measured, alone:
+//   forward of BF16 rows with delta, h, y and an 8-bit checkpoint
+//     16384 x 4096   97 us    6.2 TB/s      8 x 4096   3.8 us
+//   forward of FP32 rows with delta, h, y cast to MX and a checkpoint
+//     4096 x 12288  120 us    5.1 TB/s
+//   backward from the checkpoint, with the stream's gradient, BF16
+//     8192 x 5120    59 us    5.0 TB/s      16384 x 4096   82 us   5.7 TB/s
+//   backward from FP32 rows of odd length, whose slots straddle 16 bytes
+//     1000 x 1003   6.8 us, and 4.2 us for the sums of the columns
+// (a copy of 1 GiB reads and writes 5.1 TB/s; sizes that the last level of
+// cache holds go above that).
 #include "norm_common.h"
 #include "norm_shape.h"
 
@@ -27,7 +39,7 @@ constexpr int kWaveRows = 4;   // rows of a workgroup when a wave has a row of i
 // each, thread t the slots t, t + threads, ...  Workgroups stay for several
 // rows with gamma in registers, and the next row's loads go out before the
 // present row's sum.  K = 4 (rows above 16384 columns) has registers for
-// neither.
+// neither: 4096 x 20480 FP32 221 us, 4.9 TB/s.
 template <int IN, int K, bool WAVE, bool TINY>
 __global__ __launch_bounds__(WAVE ? 256 : K == 2 || K == 4 ? 1024 : 512,
                              rms_fwd_waves(K, IN == kInF32) / 4) void k_rms_fwd(const RmsFwd p) {
@@ -157,7 +169,10 @@ __global__ __launch_bounds__(WAVE ? 256 : K == 2 || K == 4 ? 1024 : 512,
 // again for dx.  The next row's dy and h (or checkpoint) go out before the
 // present row is worked on; the stream's gradient, needed only at the end of
 // a row, before the row's sum.  K = 4 (rows above 16384 columns) has room
-// neither for the next row nor for gamma.
+// neither for the next row nor for gamma, and keeps the columns' sums in LDS,
+// where they are its threads' own words: 4096 x 20480 FP32 343 us (3.4 TB/s)
+// against 445 with the sums in registers, some of which spill, and 366 with
+// eight slots to each of half the threads.
 // HELD: the checkpoint's format, or kNotHeld.
 constexpr int kNotHeld = -1;
 template <int IN, int HELD, bool TINY>
@@ -215,6 +230,8 @@ __global__ __launch_bounds__(kRmsBwdThreads) void k_rms_bwd(
   constexpr bool AHEAD = K <= 2;
   __shared__ float red[2][16];
   extern __shared__ float sums[];            // [groups - 1][8][nt]
+  // K = 4: the columns' sums, a thread's own words
+  __shared__ float4 own[AHEAD ? 1 : 2 * K * kRmsBwdThreads];
   // a wave is of one group
   const int group = __builtin_amdgcn_readfirstlane((int)threadIdx.x / nt);
   const int thread = threadIdx.x - group * nt;
@@ -222,13 +239,18 @@ __global__ __launch_bounds__(kRmsBwdThreads) void k_rms_bwd(
   const int tiles = (p.cols + 127) >> 7;
   const float inv_n = 1.0f / (float)p.cols;
   const int64_t step = (int64_t)gridDim.x * groups;
-  float g[AHEAD ? K : 1][8], dg[K][8];
+  float g[AHEAD ? K : 1][8], dg[AHEAD ? K : 1][8];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int slot = thread + k * nt;
-    if constexpr (AHEAD) load_weight8<TINY>(p.gamma, p.w_type, slot * 8, p.cols, g[k]);
+    if constexpr (AHEAD) {
+      load_weight8<TINY>(p.gamma, p.w_type, slot * 8, p.cols, g[k]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dg[k][i] = 0.0f;
+      for (int i = 0; i < 8; ++i) dg[k][i] = 0.0f;
+    } else {
+      own[2 * k * kRmsBwdThreads + thread] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      own[(2 * k + 1) * kRmsBwdThreads + thread] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
   }
   RmsSlot<IN, HELD, TINY> in[K], ahead[AHEAD ? K : 1];
   Slot<IN> res[K];
@@ -273,9 +295,20 @@ __global__ __launch_bounds__(kRmsBwdThreads) void k_rms_bwd(
         const float unit = in[k].get(rstd, dy, v);
         float a = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          a += dy[i] * gk[i] * v[i];
-          dg[k][i] += dy[i] * (HELD != kNotHeld ? unit * v[i] : v[i]);
+        for (int i = 0; i < 8; ++i) a += dy[i] * gk[i] * v[i];
+        const auto gain = [&](int i) {
+          return dy[i] * (HELD != kNotHeld ? unit * v[i] : v[i]);
+        };
+        if constexpr (AHEAD) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dg[k][i] += gain(i);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float4& o = own[(2 * k + j) * kRmsBwdThreads + thread];
+            o = make_float4(o.x + gain(4 * j), o.y + gain(4 * j + 1), o.z + gain(4 * j + 2),
+                            o.w + gain(4 * j + 3));
+          }
         }
         s += unit * a;
         __builtin_amdgcn_sched_barrier(0);   // one slot widened at a time
@@ -321,9 +354,9 @@ __global__ __launch_bounds__(kRmsBwdThreads) void k_rms_bwd(
       }
     }
   }
-  if (groups > 1) {
+  if (AHEAD && groups > 1) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+    for (int k = 0; k < (AHEAD ? K : 0); ++k) {
       __syncthreads();
       if (group > 0) {
 #pragma unroll
@@ -343,12 +376,22 @@ __global__ __launch_bounds__(kRmsBwdThreads) void k_rms_bwd(
   for (int k = 0; k < K; ++k) {
     const int slot = thread + k * nt;
     const int nv = p.cols - slot * 8;
-    if (nv > 0) store_f32x8(out + slot * 8, dg[k], nv);
+    auto& to = dg[AHEAD ? k : 0];
+    if constexpr (!AHEAD) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float4 o = own[(2 * k + j) * kRmsBwdThreads + thread];
+        to[4 * j] = o.x, to[4 * j + 1] = o.y, to[4 * j + 2] = o.z, to[4 * j + 3] = o.w;
+      }
+    }
+    if (nv > 0) store_f32x8(out + slot * 8, to, nv);
   }
 }
 
 // dgamma from n rows of partial sums (at most 256): 16 columns a workgroup,
-// 64 threads a column, in an order that does not depend on timing.
+// 64 threads a column, in an order that does not depend on timing.  A launch
+// of its own: what has to be added is not there before the last row, and
+// counting workgroups in memory would need it cleared first.
 __global__ __launch_bounds__(1024) void k_rms_bwd_sum(const float* __restrict__ part, int n,
                                                       int cols, float* __restrict__ dgamma) {
   __shared__ float red[64][16];

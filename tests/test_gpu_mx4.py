@@ -64,6 +64,21 @@ def test_both_ways(F, rows, cols):
     assert torch.equal(oT, qT) and torch.equal(osT, sT)
 
 
+@pytest.mark.parametrize("rows,cols", [(8160, 2080), (2048, 8192), (131072, 160), (32, 65568)])
+def test_both_ways_of_large_tensors(F, rows, cols):
+    """Tall tiles, whole and cut off at both edges: as the cast along rows, of
+    x and of x^T."""
+    x = sample(rows, cols).to(DEV)
+    x[5, 7], x[rows - 1, cols - 1], x[rows // 2, 0] = float("nan"), float("inf"), -float("inf")
+    x[:, 32:64] = 0
+    q, s, qT, sT = cast(F, x)
+    for got, want in zip((q, s, qT, sT), cast(F, x, False) + cast(F, x.t().contiguous(), False)):
+        assert torch.equal(got, want)
+    oT, osT = u8(cols, rows // 2), u8(cols, rows // 32)
+    F.fp8_quantize_mx4_t(x, None, None, oT, osT)
+    assert torch.equal(oT, qT) and torch.equal(osT, sT)
+
+
 def test_every_value(F):
     """Every BF16 value beside one that gives its block a scale: alone, where
     it is the largest, and under larger ones, ties among them."""
