@@ -22,8 +22,37 @@ TileSize size_of(TileKind t) {
 }
 
 // The tile, from the rows that a segment has on average and the tiles that
-// there are.
-TileKind choose(const SegProblem& q) {
+// there are.  While segments are short, every expert's weights are read once
+// per tile row, so what counts is how many bytes are on their way and that no
+// tile row is mostly empty; with long ones, how often the operands are read.
+// Measured (us; rows by expert, 2 of 8 experts a token, 4096 -> 11008):
+//   tokens  rows of      per-tensor scales               4-bit weights, MX
+//           a segment    16x64 32x64 64x64 64x128 128 256   16x64 32x64 64x64 128
+//     16        4           76    73    79         103 122     45    48    53  72
+//    128       32                90    90    86  106
+//    256       64                     100    91  103 122
+//    512      128                            117  128 125
+//   1024      256                            180  164 170
+//   1536      384                            243  195 179
+//   2048      512                            313  264 226
+//   4096     1024                            579  461 391
+// and dense, 11008 x 4096 weights of 4 bits, 8-bit rows:
+//   M             1          64               128              256
+//   16x64       8.7
+//   32x64      11.5
+//   64x64      12.9        13.4              17.6             23.9
+//   64x128                 16.0              16.6             22.5
+//   128                    25.9              26.6             27.6
+//   M           512         768              1024
+//   64x128     37.8        58.4                73
+//   128        35.3        59.0                62
+//   256        52.9          54                56
+// So 16 rows under 4-bit weights (8-bit ones gain nothing from it: they are
+// twice the bytes a row, and 32 rows read them as fast), 32, and 256 and 128
+// where segments fill them and there are tiles for the CUs; between them 64 x
+// 128, or 64 x 64 where those are too few.  64 experts of 2000 x 1408, 6 a
+// token, 1000 tokens (94 rows): 64x128 60, 64x64 69, 128 59, 256 74.
+TileKind by_rows(const SegProblem& q) {
   const int64_t mean = (q.M + q.experts - 1) / q.experts;
   const auto at_least = [&](TileKind t, int64_t n) {
     return row_tiles(q, size_of(t).rows, size_of(t).columns) >= n;
@@ -33,6 +62,14 @@ TileKind choose(const SegProblem& q) {
   if (mean > 320 && at_least(kTile256, 160)) return kTile256;
   if (mean > 176 && at_least(kTile128, 256)) return kTile128;
   return at_least(kTile64x128, 160) ? kTile64x128 : kTile64;
+}
+// A larger one where the grid would be.
+TileKind choose(const SegProblem& q) {
+  int t = by_rows(q);
+  while (t < kTile256 &&
+         row_tiles(q, size_of((TileKind)t).rows, size_of((TileKind)t).columns) > kMaxGrid - 7)
+    ++t;
+  return (TileKind)t;
 }
 
 hipError_t launch_rows(const SegProblem& q, TileKind t, hipStream_t s) {

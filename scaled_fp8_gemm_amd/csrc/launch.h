@@ -304,7 +304,8 @@ inline bool unaligned(const SegProblem& q) {
 hipError_t launch_gemm_grouped(const SegProblem& p, bool depth, hipStream_t s);
 hipError_t launch_gemm_fp4(const SegProblem& p, hipStream_t s);
 // Their kernels, by the output tile's rows (x columns, where they differ by
-// more than the kind says: 16 and 32 rows have 64).  kTile16: 4-bit weights.
+// more than the kind says: 16 and 32 rows have 64), in the order of their
+// sizes.  kTile16: 4-bit weights.
 enum TileKind { kTile16, kTile32, kTile64, kTile64x128, kTile128, kTile256 };
 hipError_t launch_seg_tensor(const SegProblem& p, TileKind t, hipStream_t s);
 hipError_t launch_seg_mx(const SegProblem& p, TileKind t, hipStream_t s);

@@ -318,3 +318,25 @@ def test_more_than_2_31_elements(F, orc, lengths):
                              torch.tensor(offsets, dtype=torch.int32, device=DEV), 2, rows, n, k, y)
     a, b = G.values(x[-3:], xs[-3:], 0, MX), G.values(w[-5:], ws[-5:], E2M1, MX)
     G.check(orc, y[-3:, -5:].contiguous(), a, b, "last")
+
+
+def test_more_tiles_than_a_grid(F, orc):
+    """1024 experts of one row and so many columns that the small tiles which
+    one row would have are more than a grid: every expert's row, at both ends
+    of the columns and at tiles' edges."""
+    experts, n, k = 1024, 262400, 16
+    g = torch.Generator(device=DEV).manual_seed(4)
+    w = torch.randint(0, 64, (experts, n, k), generator=g, device=DEV, dtype=torch.uint8)
+    x = torch.randint(0, 64, (experts, k), generator=g, device=DEV, dtype=torch.uint8)
+    sx, sw = torch.ones(1, device=DEV), torch.full((experts,), 0.5, device=DEV)
+    off = torch.arange(experts + 1, dtype=torch.int32, device=DEV)
+    y = unwritten(experts, n)
+    F.fp8_gemm_grouped_fprop(F.operand(x, 0, TENSOR, sx), F.operand(w, 0, TENSOR, sw), off,
+                             experts, experts, n, k, y)
+    cols = some_columns(n)
+    some, a = w[:, cols].cpu(), G.values(x, sx, 0, TENSOR)
+    got = y[:, cols].cpu()
+    for e in (0, 1, 500, 1022, 1023):
+        b = G.values(some[e], sw[:1].cpu(), 0, TENSOR)
+        G.check(orc, got[e:e + 1].to(DEV), a[e:e + 1], b, f"expert {e}")
+    assert not (y == -777.0).any()
