@@ -72,6 +72,24 @@ TileKind choose(const SegProblem& q) {
   return (TileKind)t;
 }
 
+// Weight gradients: 256 x 256 where the outputs fill a CU each with one, and
+// 64 x 64 where they do not or leave most of such a tile empty (us; MX, 2
+// experts a token):
+//   experts  outputs       tokens   256x256  64x64
+//      8     512 x 768       8192      56      24
+//      8     1024 x 1024     8192      59      45
+//      8     1024 x 1280     8192      78      62   (blockwise)
+//      8     1408 x 1792     8192      88      98
+//      8     1408 x 1792     1000      26      29   (per tensor)
+//     64     512 x 300       8192      32      21
+//    128     384 x 300       8192      44      30
+// 128 x 128 lies between them; long outputs lose by it also where segments are
+// short (1000 tokens to 6 of 64 experts, 2000 x 1408: 106 to 121 against 116;
+// 256 tokens to 2 of 8, 4096 x 11008: 193 against 178).
+TileKind choose_depth(const SegProblem& q) {
+  return q.M * q.N * q.experts >= 256 * 256 * 256 ? kTile256 : kTile64;
+}
+
 hipError_t launch_rows(const SegProblem& q, TileKind t, hipStream_t s) {
   if (q.fb == 4) return launch_seg_fp4(q, t, s);
   if (q.mode == 0) return launch_seg_tensor(q, t, s);
@@ -82,7 +100,7 @@ hipError_t launch_rows(const SegProblem& q, TileKind t, hipStream_t s) {
 
 hipError_t launch_gemm_grouped(const SegProblem& q, bool depth, hipStream_t s) {
   if (q.M == 0 || q.N == 0) return hipSuccess;
-  return depth ? launch_seg_depth(q, s) : launch_rows(q, choose(q), s);
+  return depth ? launch_seg_depth(q, choose_depth(q), s) : launch_rows(q, choose(q), s);
 }
 
 hipError_t launch_gemm_fp4(const SegProblem& q0, hipStream_t s) {

@@ -49,6 +49,7 @@ struct SegArgs {
   Args g;                  // M: rows of A; C: of expert 0
   const int32_t* offsets;  // or NULL: one segment
   int experts;
+  bool stream;             // C is written past the caches
 };
 
 // Tile rows of segment e, and where it lies; never outside [0, rows).
@@ -234,6 +235,24 @@ __device__ __forceinline__ v8i fragment(const uint8_t* __restrict__ s, int row0,
     o[4] = hi.x; o[5] = hi.y; o[6] = hi.z; o[7] = hi.w;
   }
   return o;
+}
+
+// 16 bytes of outputs.  `stream`: so many are written in all (kStreamBytes) that a
+// later reader would not find them in a cache; past the caches, they leave
+// the operands there.  8192 tokens to 2 of 8 experts, 4096 -> 11008: the
+// weight gradient 813 -> 784 us; 1000 tokens to 6 of 64 experts, 2000 x 1408
+// each: 135 -> 114; dense 8192 x 16384 x 1024 with 4-bit operands 154 -> 127.
+template <class V>
+__device__ __forceinline__ void store16(void* to, V v, bool stream) {
+  static_assert(sizeof(V) == 16, "a chunk");
+  V* at = static_cast<V*>(to);
+  if (stream) {
+    asm volatile("");      // keeps the branch's two stores from becoming one
+    __builtin_nontemporal_store(v, at);
+    asm volatile("");
+  } else {
+    *at = v;
+  }
 }
 
 // The output tile, its waves (each a part of the tile), the LDS stages, and the
@@ -533,11 +552,59 @@ void k_gemm_seg(SegArgs p) {
       for (int r = t / CH; r < PART; r += PASS) {
         const int64_t m = m0 + part * PART + r, n = n0 + ch * 8;
         if (m < m_end && n < out.N)
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out.C) + m * out.N + n) =
-              *reinterpret_cast<const uint4*>(stage + r * ROW + ((ch ^ (r & (CH - 1))) << 4));
+          store16(static_cast<uint16_t*>(out.C) + m * out.N + n,
+                  *reinterpret_cast<const v4i*>(stage + r * ROW + ((ch ^ (r & (CH - 1))) << 4)),
+                  p.stream);
       }
     }
     return;
+  }
+  if constexpr (DEPTH) {
+    if (out.out != 0 && (out.N & 3) == 0) {
+      // FP32, in the same way: the gradients above 961 -> 895 and 207 -> 165 us,
+      // added to what is there 1160 -> 1153 and 382 -> 330
+      constexpr int PART = BM < 128 ? BM : 128, CH = BN / 4, ROW = BN * 4, PASS = NT / CH;
+      static_assert(PART * ROW <= STAGES * STAGE, "the staged rows");
+      uint8_t* stage = &lds[0][0];
+#pragma unroll
+      for (int part = 0; part < BM / PART; ++part) {
+        if (part > 0) __syncthreads();
+        if (wm * WM / PART == part) {
+#pragma unroll
+          for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+              const int r = (wm * WM) % PART + f * 16 + lr, ch = (wn * WN + j * 16) / 4 + g;
+              *reinterpret_cast<v4f*>(stage + r * ROW + ((ch ^ (r & (CH - 1))) << 4)) =
+                  acc[f][j] * s;
+            }
+        }
+        __syncthreads();
+        const int t = threadIdx.x, ch = t % CH;
+        constexpr int U = PART / PASS < 4 ? PART / PASS : 4;   // rows whose old values come together
+        float* const to = static_cast<float*>(out.C) + (m0 + part * PART) * out.N + n0 + ch * 4;
+        const bool in = n0 + ch * 4 < out.N;
+        for (int r0 = t / CH; r0 < PART; r0 += U * PASS) {
+          v4f old[U] = {};
+          if (out.out == 2) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int r = r0 + u * PASS;
+              if (in && m0 + part * PART + r < m_end)
+                old[u] = *reinterpret_cast<const v4f*>(to + r * out.N);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * PASS;
+            v4f v = *reinterpret_cast<const v4f*>(stage + r * ROW + ((ch ^ (r & (CH - 1))) << 4));
+            if (out.out == 2) v = old[u] + v;
+            if (in && m0 + part * PART + r < m_end) store16(to + r * out.N, v, p.stream);
+          }
+        }
+      }
+      return;
+    }
   }
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
@@ -570,7 +637,7 @@ typedef Tile<64, 64, 2, 2, 3> T64;
 typedef Tile<32, 64, 1, 4, 4> T32;
 typedef Tile<16, 64, 1, 4, 3, 256> T16;
 
-inline SegArgs seg_args(const SegProblem& q, int bm, int bn) {
+inline SegArgs seg_args(const SegProblem& q, int bm, int bn, bool depth) {
   SegArgs a;
   a.g.A = q.A; a.g.B = q.B; a.g.sa = q.sa; a.g.sb = q.sb; a.g.C = q.C; a.g.out = q.out;
   a.g.Cq = q.Cq; a.g.q_scale = q.q_scale; a.g.q_fmt = q.q_fmt; a.g.part = q.part;
@@ -579,12 +646,13 @@ inline SegArgs seg_args(const SegProblem& q, int bm, int bn) {
   a.g.tiles_n = (int)((q.N + bn - 1) / bn);
   a.offsets = q.offsets;
   a.experts = q.experts;
+  a.stream = q.M * q.N * (depth ? q.experts : 1) * (q.out == 0 ? 2 : 4) > kStreamBytes;
   return a;
 }
 
 template <int MODE, int FA, int FB, int BRB, class T, bool DEPTH, bool DIRECT>
 hipError_t run(const SegProblem& q, hipStream_t s) {
-  const SegArgs a = seg_args(q, T::BM, T::BN);
+  const SegArgs a = seg_args(q, T::BM, T::BN, DEPTH);
   const int64_t n = DEPTH ? ((int64_t)a.g.tiles_m * a.g.tiles_n + 7) / 8 * 8 * q.experts
                           : (row_tiles(q, T::BM, T::BN) + 7) / 8 * 8;   // every XCD the same count
   if (n > kMaxGrid) return hipErrorInvalidConfiguration;

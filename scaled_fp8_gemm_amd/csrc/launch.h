@@ -311,6 +311,6 @@ hipError_t launch_seg_tensor(const SegProblem& p, TileKind t, hipStream_t s);
 hipError_t launch_seg_mx(const SegProblem& p, TileKind t, hipStream_t s);
 hipError_t launch_seg_block(const SegProblem& p, TileKind t, hipStream_t s);
 hipError_t launch_seg_fp4(const SegProblem& p, TileKind t, hipStream_t s);
-hipError_t launch_seg_depth(const SegProblem& p, hipStream_t s);
+hipError_t launch_seg_depth(const SegProblem& p, TileKind t, hipStream_t s);
 
 }  // namespace fp8sg

@@ -183,21 +183,25 @@ def run_depth(F, orc, lengths, n, k, scaling, fa, fb, out="bf16", after=0, unit=
     off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
     old = torch.zeros(e, n, k)
     if out == "bf16":
-        dw = unwritten(e, n, k)
+        dw = unwritten(e, n, k) * float("nan")
         F.fp8_gemm_grouped_wgrad(ao, bo, off, e, rows, n, k, dw)
     else:
-        dw = unwritten(e, n, k, dtype=torch.float32)
+        dw = unwritten(e, n, k, dtype=torch.float32) * float("nan")
         if out == "add":
             old = torch.randn(e, n, k, generator=torch.Generator().manual_seed(9))
             dw.copy_(old)
         F.fp8_gemm_grouped_wgrad_f32(ao, bo, off, e, rows, n, k, dw, accumulate=out == "add")
     av, bv = G.values(*a, fa, scaling), G.values(*b, fb, scaling)
+    m, c = (some_columns(n), some_columns(k)) if n * k > 1 << 20 else (range(n), range(k))
+    av, bv = av[list(m)], bv[list(c)]
+    got, old = dw[:, list(m)][:, :, list(c)], old[:, list(m)][:, :, list(c)]
     for i in range(e):
         r = slice(offsets[i], offsets[i + 1])
         if out == "bf16":
-            G.check(orc, dw[i], av[:, r], bv[:, r], f"expert {i}")
+            G.check(orc, got[i].contiguous(), av[:, r], bv[:, r], f"expert {i}")
         else:
-            G.check_f32(dw[i], old[i], av[:, r], bv[:, r], f"expert {i}")
+            G.check_f32(got[i], old[i], av[:, r], bv[:, r], f"expert {i}")
+    assert not dw.isnan().any()                      # every output written
     return dw
 
 
@@ -212,6 +216,23 @@ def test_wgrad(F, orc, scaling, fa, fb, out):
 def test_wgrad_sizes(F, orc, n, k):
     run_depth(F, orc, [1, 0, 3], n, k, MX, 0, 0)
     run_depth(F, orc, [3, 1, 0, 9], n, k, TENSOR, 1, 0, unit=16, after=3)
+
+
+# whole float4s of an FP32 result in tiles of 64; tiles of 256, with rows of any
+# length too; results that are written past the caches
+@pytest.mark.parametrize("lengths,n,k", [([2, 0, 1, 5], 130, 72), ([2, 0, 1, 3, 1, 0, 1, 1], 1300, 1616),
+                                         ([2, 0, 1, 1, 1, 0, 1, 1], 1300, 1615),
+                                         ([0, 1, 1, 0, 1, 0, 2, 1], 2900, 2904)])
+@pytest.mark.parametrize("scaling,fa,fb", [(TENSOR, 1, 0), (TENSOR, 0, 0), (BLOCK, 0, 1), (MX, 0, 0),
+                                           (MX, 1, 1)])
+@pytest.mark.parametrize("out", ["bf16", "f32", "add"])
+def test_wgrad_tiles(F, orc, lengths, n, k, scaling, fa, fb, out):
+    run_depth(F, orc, lengths, n, k, scaling, fa, fb, out, after=1)
+
+
+@pytest.mark.parametrize("sa,fb", [(TENSOR, 0), (BLOCK, 0), (MX, E2M1)])
+def test_rows_written_past_the_caches(F, orc, sa, fb):
+    run_rows(F, orc, [700, 90, 513], 52104, 128, sa, sa, 0, fb, after=5)
 
 
 def test_wgrad_without_rows(F):
@@ -330,7 +351,7 @@ def test_more_tiles_than_a_grid(F, orc):
     x = torch.randint(0, 64, (experts, k), generator=g, device=DEV, dtype=torch.uint8)
     sx, sw = torch.ones(1, device=DEV), torch.full((experts,), 0.5, device=DEV)
     off = torch.arange(experts + 1, dtype=torch.int32, device=DEV)
-    y = unwritten(experts, n)
+    y = unwritten(experts, n) * float("nan")
     F.fp8_gemm_grouped_fprop(F.operand(x, 0, TENSOR, sx), F.operand(w, 0, TENSOR, sw), off,
                              experts, experts, n, k, y)
     cols = some_columns(n)
@@ -339,4 +360,4 @@ def test_more_tiles_than_a_grid(F, orc):
     for e in (0, 1, 500, 1022, 1023):
         b = G.values(some[e], sw[:1].cpu(), 0, TENSOR)
         G.check(orc, got[e:e + 1].to(DEV), a[e:e + 1], b, f"expert {e}")
-    assert not (y == -777.0).any()
+    assert not y.isnan().any()                       # every output written
