@@ -623,7 +623,7 @@ void k_gemm_seg(SegArgs p) {
 }
 
 // The tiles by TileKind; which one is taken, and the times of its neighbours,
-// stand in gemm_grouped.hip.  Large ones read their operands as few times as
+// stand in seg_shape.h.  Large ones read their operands as few times as
 // LDS allows.  The smaller ones are for short segments, where loading is all:
 // several workgroups a CU, two or three steps on their way beside the one at
 // work (16 tokens to 8 experts with 4-bit weights: 96 us with one step on its
@@ -654,8 +654,9 @@ inline SegArgs seg_args(const SegProblem& q, int bm, int bn, bool depth) {
 template <int MODE, int FA, int FB, int BRB, class T, bool DEPTH, bool DIRECT>
 hipError_t run(const SegProblem& q, hipStream_t s) {
   const SegArgs a = seg_args(q, T::BM, T::BN, DEPTH);
+  // every XCD the same count
   const int64_t n = DEPTH ? ((int64_t)a.g.tiles_m * a.g.tiles_n + 7) / 8 * 8 * q.experts
-                          : (row_tiles(q, T::BM, T::BN) + 7) / 8 * 8;   // every XCD the same count
+                          : (row_tiles(q.size(), T::BM, T::BN) + 7) / 8 * 8;
   if (n > kMaxGrid) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((k_gemm_seg<MODE, FA, FB, BRB, T, DEPTH, DIRECT>), dim3((unsigned)n),
                      dim3(T::NT), 0, s, a);

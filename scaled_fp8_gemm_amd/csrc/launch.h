@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "seg_shape.h"
+
 namespace fp8sg {
 
 int device_cu_count();
@@ -289,24 +291,15 @@ hipError_t launch_gemm_mx_k32(const GemmProblem& p, hipStream_t s);
 struct SegProblem : GemmProblem {
   const int32_t* offsets = nullptr;   // device, experts + 1
   int experts = 1;
+  SegSize size() const { return {M, N, experts, offsets != nullptr, fb == 4}; }
 };
-// The most tiles of bm x bn that the rows can have: with offsets at most one
-// tile row more a segment than the rows alone would need.
-inline int64_t row_tiles(const SegProblem& q, int bm, int bn) {
-  const int64_t tn = (q.N + bn - 1) / bn;
-  if (!q.offsets) return (q.M + bm - 1) / bm * tn;
-  return (q.M / bm + (q.M < q.experts ? q.M : q.experts)) * tn;
-}
 // E8M0 bytes that are not aligned dwords of four blocks.
 inline bool unaligned(const SegProblem& q) {
   return q.K % 128 != 0 || (((uintptr_t)q.sa | (uintptr_t)q.sb) & 3) != 0;
 }
 hipError_t launch_gemm_grouped(const SegProblem& p, bool depth, hipStream_t s);
 hipError_t launch_gemm_fp4(const SegProblem& p, hipStream_t s);
-// Their kernels, by the output tile's rows (x columns, where they differ by
-// more than the kind says: 16 and 32 rows have 64), in the order of their
-// sizes.  kTile16: 4-bit weights.
-enum TileKind { kTile16, kTile32, kTile64, kTile64x128, kTile128, kTile256 };
+// Their kernels, by the output tile.
 hipError_t launch_seg_tensor(const SegProblem& p, TileKind t, hipStream_t s);
 hipError_t launch_seg_mx(const SegProblem& p, TileKind t, hipStream_t s);
 hipError_t launch_seg_block(const SegProblem& p, TileKind t, hipStream_t s);
