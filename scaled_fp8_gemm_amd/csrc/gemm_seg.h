@@ -75,20 +75,12 @@ __device__ __forceinline__ int lane_value(int v, int lane) {
 }
 
 // One output tile: expert, its rows [from, to) and the tile's place among
-// `count` tile rows and the tile columns.  `at`: the workgroup's number, dealt
-// out in contiguous ranges to the XCDs (XCD) or as it is.
+// `count` tile rows and the tile columns.  `at`: the workgroup's number; the
+// XCDs, which take workgroups in turn, get contiguous ranges of the tiles.
 struct Place {
   int e, from, to, count, local;
 };
 template <int BM>
-__device__ __forceinline__ int tile_rows(const SegArgs& p) {
-  if (p.offsets == nullptr) return p.g.tiles_m;
-  int total = 0, from, to;
-  for (int c = 0; c < p.experts; c += 64)
-    total += lane_value(wave_scan(tiles_of(p, c + (int)(threadIdx.x & 63), BM, from, to)), 63);
-  return total;
-}
-template <int BM, bool XCD>
 __device__ __forceinline__ bool find(const SegArgs& p, int tiles_n, int at, Place& w) {
   const int lane = threadIdx.x & 63;
   int from, to, n = 0, upto = 0, total = 0;
@@ -103,7 +95,7 @@ __device__ __forceinline__ bool find(const SegArgs& p, int tiles_n, int at, Plac
   }
   const int T = total * tiles_n;
   int t = at;
-  if constexpr (XCD) {
+  {                                            // its XCD's range
     const int per = (T + 7) / 8;
     if ((at >> 3) >= per) return false;
     t = (at & 7) * per + (at >> 3);
@@ -304,7 +296,7 @@ void k_gemm_seg(SegArgs p) {
     at.from = min(max(p.offsets[at.e], 0), rows) / unit * unit;
     at.to = max(min(p.offsets[at.e + 1], rows) / unit * unit, at.from);
   } else {
-    if (!find<BM, true>(p, p.g.tiles_n, blockIdx.x, at)) return;
+    if (!find<BM>(p, p.g.tiles_n, blockIdx.x, at)) return;
     walk(at.local, at.count, p.g.tiles_n, tm, tn);
   }
   const int64_t n0 = (int64_t)tn * BN;
