@@ -553,7 +553,8 @@ fp8_status_t fp8_layernorm_bwd(const void* dy_bf16, const void* x, int32_t x_typ
 /* The addition to the residual stream and root-mean-square norm:
  * h = x + delta (x without delta), rounded to x's type;
  * rstd = 1 / sqrt(sum_j h_j^2 / cols + eps), xhat = h rstd, y = xhat gamma, in
- * FP32, from h as rounded.
+ * FP32 (the sum of the squares too: past FP32's range rstd is 0), from h as
+ * rounded.
  *   x            [rows][cols] of x_type (fp8_type_t), 1 <= cols <= 32768
  *   delta_bf16   [rows][cols] BF16, nullable
  *   gamma        [cols] of w_type (fp8_type_t)

@@ -75,6 +75,16 @@ inline int64_t row_tiles(const SegSize& q, TileKind t) {
 // where segments fill them and there are tiles for the CUs; between them 64 x
 // 128, or 64 x 64 where those are too few.  64 experts of 2000 x 1408, 6 a
 // token, 1000 tokens (94 rows): 64x128 60, 64x64 69, 128 59, 256 74.
+// What the rule does not see: M = 768 above has 129 tiles of 256 x 256, less
+// than the 160 that it asks for, and gets 128 x 128.  And neither the depth
+// nor, up to 24 rows, the number of tiles: 4096 columns are 64 workgroups,
+// with 4-bit weights
+//   columns x depth       4096 x 11008   4096 x 4096   11008 x 4096
+//   8-bit rows, 16x64         17.5           8.0            8.4
+//               32x64         25.1          11.0           11.6
+//   4-bit rows, 16x64         12.6           6.5            7.2
+//               32x64         17.2           8.3            8.7
+// (M = 1; 16 rows the same within 0.3).
 inline TileKind by_rows(const SegSize& q) {
   const int64_t mean = (q.M + q.experts - 1) / q.experts;
   const auto at_least = [&](TileKind t, int64_t n) { return row_tiles(q, t) >= n; };
@@ -93,9 +103,8 @@ inline TileKind choose_rows(const SegSize& q, int64_t grid, int64_t words) {
   return words && row_tiles(q, (TileKind)t) > words ? kTile256 : (TileKind)t;
 }
 
-// Weight gradients: 256 x 256 where the outputs fill a CU each with one, and
-// 64 x 64 where they do not or leave most of such a tile empty (us; MX, 2
-// experts a token):
+// Weight gradients: 256 x 256 where all outputs together are a tile's for each
+// CU, else 64 x 64 (us; MX, 2 experts a token):
 //   experts  outputs       tokens   256x256  64x64
 //      8     512 x 768       8192      56      24
 //      8     1024 x 1024     8192      59      45
@@ -104,6 +113,15 @@ inline TileKind choose_rows(const SegSize& q, int64_t grid, int64_t words) {
 //      8     1408 x 1792     1000      26      29   (per tensor)
 //     64     512 x 300       8192      32      21
 //    128     384 x 300       8192      44      30
+//     64     128 x 2048      8192      29      30
+//    256     1000 x 1000     8192     191     305
+// It is the total alone that decides, not how much of its tiles an expert
+// fills: many experts whose outputs leave 256 x 256 tiles mostly empty pass the
+// bound, and lose by it:
+//    256     384 x 300       8192      89      54
+//    256     384 x 300       8192      83      39   (per tensor)
+//    128     2048 x 64       8192      46      35
+//    128     64 x 4032       8192      82      77
 // 128 x 128 lies between them; long outputs lose by it also where segments are
 // short (1000 tokens to 6 of 64 experts, 2000 x 1408: 106 to 121 against 116;
 // 256 tokens to 2 of 8, 4096 x 11008: 193 against 178).
