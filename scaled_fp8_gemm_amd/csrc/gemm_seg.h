@@ -22,11 +22,12 @@
 // What bounds it, and measured times:
 //   long segments: the matrix cores, whose clock falls to 1.9 GHz under such
 //     products.  8192 tokens to 2 of 8 experts, 4096 -> 11008, blockwise
-//     scales 760 us (1944 TFLOP/s), its weight gradient under MX 765 us (1930);
-//     4096 x 49152 x 12288 with both operands in 4 bits 1224 us (4040), where
-//     LDS reads and the operands' loads bound it too (the MFMAs are busy 48 %
-//     of the time, LDS 37 %; without the loads of operands it would take 22 %
-//     less, without those of scales 5 %, without B's LDS reads 7 %).
+//     scales 760 to 779 us (1944 TFLOP/s), its weight gradient under MX 765 us
+//     (1930); 4096 x 49152 x 12288 with both operands in 4 bits 1224 to 1258 us
+//     (4040), where LDS reads and the operands' loads bound it too (the MFMAs
+//     are busy 46 to 48 % of the time, LDS 37 %; without the loads of operands
+//     it would take 22 % less, without those of scales 5 %, without B's LDS
+//     reads 7 %).
 //   short segments: the weights' bytes.  16 tokens to 2 of 8 experts, 4096 ->
 //     11008, 4-bit weights 41.5 us (4.6 TB/s); 1000 tokens to 6 of 64 experts,
 //     2000 -> 1408, 57.7 us (3.6 TB/s; 480 tokens, which have one tile row an
